@@ -17,6 +17,11 @@
  *                                      lsa_hybrid_attn   (sink + window and sparse rows on two streams,
  *                                                         merged by log-sum-exp)
  *                                      lsa_msa_attn      (each head group over its own blocks)
+ *   Around the latent cache:
+ *                                      lsa_norm_rope     (norms of queries and keys, with the position rotation)
+ *                                      lsa_cache_append  (a step's rows normed, rotated and written to the caches)
+ *                                      lsa_prefix_attn   (dense attention of a batch behind one shared prefix)
+ *                                      lsa_rope_freqs    (host: the rotation's frequencies)
  *   Scratch sizes: lsa_workspace_size and the per-call *_workspace_size functions.
  *
  * Conventions shared by every call
@@ -67,6 +72,23 @@ typedef enum {
   LSA_OP_BUCKET_MIN = 5, /* the smaller lsa_bucket_select workspace: CUDA-core representative scoring */
   LSA_OP_HYBRID_ATTN = 6
 } lsa_op;
+
+typedef enum {
+  LSA_NORM_NONE = 0,
+  LSA_NORM_RMS = 1,   /* x / sqrt(mean x^2 + eps) * weight                          */
+  LSA_NORM_LAYER = 2  /* (x - mean x) / sqrt(var x + eps) * weight + bias           */
+} lsa_norm;
+
+typedef enum {
+  LSA_ROPE_INTERLEAVED = 0, /* pairs (2i, 2i + 1)   */
+  LSA_ROPE_HALF = 1         /* pairs (i, i + R / 2) */
+} lsa_rope_layout;
+
+typedef enum {
+  LSA_ROPE_PLAIN = 0,
+  LSA_ROPE_LINEAR = 1, /* every frequency divided by the factor                     */
+  LSA_ROPE_YARN = 2    /* arXiv 2309.00071: slow dims divided, fast ones kept, a linear ramp between */
+} lsa_rope_scaling;
 
 /*
  * lsa_index_score -- lightning-indexer scores.
@@ -417,6 +439,80 @@ int lsa_hybrid_attn(const void* q, const void* kv, int64_t L, const int32_t* idx
                     const int32_t* count, int64_t B, int H, int d_qk, int d_v, int sink, int window,
                     const int64_t* q_pos, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
                     void* stream);
+
+/*
+ * lsa_rope_freqs -- the position rotation's angular frequencies (host memory; launches nothing).
+ *   freqs[i] = base^(-2i/R), i < R/2 (R even, 2 <= R <= 1024, base > 1), then
+ *     LSA_ROPE_LINEAR: divided by factor (>= 1);
+ *     LSA_ROPE_YARN:   (1 - r_i) f_i + r_i f_i / factor, r_i = clamp((i - low) / max(high - low, 0.001), 0, 1),
+ *                      low = max(floor(d(beta_fast)), 0), high = min(ceil(d(beta_slow)), R - 1),
+ *                      d(beta) = R ln(original_len / (2 pi beta)) / (2 ln base).
+ *   *mul = the factor of cos and sin: 0.1 ln(factor) + 1 for YaRN, else 1.  Both are written in host memory; the calls
+ *   below take freqs in device memory.
+ */
+int lsa_rope_freqs(int R, double base, int scaling, double factor, int64_t original_len, double beta_fast,
+                   double beta_slow, double* freqs, float* mul);
+
+/*
+ * lsa_norm_rope -- norm of each head row and the position rotation of a part of it, in one pass.
+ *   For token t and head h, with x the D elements at x + t*x_ldt + h*x_ldh:
+ *     n = x, or the RMS or layer norm of x over its D elements (weight, bias [D] fp32; NULL weight = ones, NULL bias =
+ *     zeros; a bias only with the layer norm, neither without a norm)
+ *     a pair (u, v) of n[rope_off : rope_off + rope_dims] -> (u c - v s, v c + u s) with c = mul cos(pos[t] freqs[i]),
+ *     s = mul sin(pos[t] freqs[i]) for pair i < rope_dims / 2 (freqs device fp64 [rope_dims / 2]; NULL: no rotation,
+ *     and rope_off, rope_dims, layout, mul and pos are not used)
+ *     y + t*y_ldt + h*y_ldh = the D results rounded once to bf16, or (LSA_FP8_E4M3) the e4m3 codes of result / scale
+ *     with y_scale[t*H + h] = max |result| / 448 (1 for a row of zeros): the index queries of lsa_index_score.
+ *   Angles are formed and reduced modulo 2 pi in 64 bits, norm statistics are 32-bit.
+ *   x bf16; x_ldt, x_ldh, y_ldt, y_ldh are strides in elements, any multiples of 8 (0 for a broadcast x).  y may be x with
+ *   the same strides (bf16); otherwise they must not overlap.  D a multiple of 8, at most 1024; rope_off a multiple of
+ *   8, rope_dims of 16.  x 16-byte aligned, y 16 bytes (bf16) or 8 (e4m3).  y_scale non-NULL for LSA_FP8_E4M3 only.
+ */
+int lsa_norm_rope(const void* x, int64_t x_ldt, int64_t x_ldh, int64_t T, int H, int D, int norm, const float* weight,
+                  const float* bias, float eps, const double* freqs, int rope_off, int rope_dims, int layout, float mul,
+                  const int64_t* pos, void* y, int64_t y_ldt, int64_t y_ldh, int dtype, float* y_scale, void* stream);
+
+/*
+ * lsa_cache_append -- a step's tokens normed, rotated and written to their slots of the caches.
+ *   For token t with slot[t] = s >= 0 (s = -1: the token is skipped, the padding of a batch):
+ *     kv[s, 0:512]   = RMS norm of a[t, 0:512] with kv_weight [512] (NULL: no norm)
+ *     kv[s, 512:576] = a[t, 512:576] rotated by pos[t] (freqs device fp64 [32]; NULL: not rotated, pos not used)
+ *   and, with k: the index key k[t] (d_I in {32, 64, 128}) normed (k_norm, k_weight, k_bias as in lsa_norm_rope), its dims
+ *   [k_rope_off, k_rope_off + 64) rotated by the same angles in k_layout (k_rope_off < 0: not rotated), written to
+ *   k_cache[s] as bf16, or as e4m3 codes with k_scale[s] (LSA_FP8_E4M3).
+ *   A slot s of a paged cache is page * page_size + offset.  Slots other than -1 must be distinct: of two tokens with one
+ *   slot, which one's bytes stay is not defined.  A slot outside [-1, n_slots) writes nothing and lsa_device_status reports
+ *   LSA_ERR_DEVICE_CHECK.  Rows without a token stay as they were.
+ *   a [T, a_ld] bf16 (a_ld a multiple of 8 elements), k [T, k_ld] bf16, slot, pos [T] int64; kv [n_slots, 576] bf16,
+ *   k_cache [n_slots, d_I], k_scale [n_slots] fp32.  a, k, kv, k_cache 16-byte aligned.  d_qk = 576, d_v = 512.
+ */
+int lsa_cache_append(const void* a, int64_t a_ld, int64_t T, int d_qk, int d_v, const float* kv_weight, float kv_eps,
+                     const double* freqs, int layout, float mul, const int64_t* pos, const int64_t* slot, void* kv,
+                     int64_t n_slots, const void* k, int64_t k_ld, int d_I, int k_norm, const float* k_weight,
+                     const float* k_bias, float k_eps, int k_rope_off, int k_layout, void* k_cache, int k_dtype,
+                     float* k_scale, void* stream);
+
+/*
+ * lsa_prefix_attn -- dense attention of a batch whose sequences share one prefix, over the latent cache.
+ *   The keys of query b are the Lp rows of `prefix` and its own own_len[b] rows: own token i is row i % page of page
+ *   table[b*table_ld + i / page].  With z = scale * q[b,h,:] . key[0:576]:
+ *     out[b,h] = sum softmax(z) key[0:512]   (bf16, fp32 accumulation)      lse[b,h] = log sum exp(z)  (natural log)
+ *   A query without any key gives out = 0, lse = -inf.  The prefix is read once for the batch, not once a sequence.
+ *   Several tokens of one sequence (speculative or chunked decoding) are several queries with the same table row and
+ *   growing own_len.
+ *   q [B, H, 576] bf16, prefix [Lp, 576] bf16, pages [n_pages, page, 576] bf16, table int32 [B, table_ld], own_len int32
+ *   [B] (NULL: no own tokens, and pages, table are not used), out [B, H, 512] bf16, lse [B, H] fp32 or NULL.
+ *   page a power of two from 8 to 65536.  Table entries behind a sequence's last page are not read.  own_len outside [0,
+ *   table_ld * page] is clamped and a page id outside [0, n_pages) reads as rows of zeros; lsa_device_status reports either
+ *   as LSA_ERR_DEVICE_CHECK.  q, prefix, pages, out 16-byte aligned.  ws: lsa_prefix_attn_workspace_size(B, H) bytes.
+ */
+int lsa_prefix_attn(const void* q, int64_t B, int H, int d_qk, int d_v, const void* prefix, int64_t Lp,
+                    const void* pages, int64_t n_pages, int page, const int32_t* table, int64_t table_ld,
+                    const int32_t* own_len, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* lsa_prefix_attn_workspace_size -- scratch bytes of lsa_prefix_attn; (size_t)-1 for invalid sizes. */
+size_t lsa_prefix_attn_workspace_size(int64_t B, int H);
 
 /*
  * lsa_workspace_size -- scratch bytes a call needs (0 if none).

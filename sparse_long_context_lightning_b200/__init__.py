@@ -8,6 +8,7 @@ the first call does, and raises ``LsaError`` if the built library is missing.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -20,6 +21,10 @@ LSA_OK = 0
 LSA_BF16 = 0
 LSA_FP8_E4M3 = 1
 LSA_OP_TOPK, LSA_OP_BUCKET, LSA_OP_ATTN, LSA_OP_REFINE, LSA_OP_BUCKET_MIN, LSA_OP_HYBRID_ATTN = 1, 2, 3, 4, 5, 6
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+_LAYOUTS = {"interleaved": 0, "half": 1}
+_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
 
 _STATUS = {0: "LSA_OK", -1: "LSA_ERR_INVALID_ARG", -2: "LSA_ERR_UNSUPPORTED", -3: "LSA_ERR_WORKSPACE",
            -4: "LSA_ERR_CUDA", -5: "LSA_ERR_DEVICE_CHECK", -6: "LSA_ERR_TIMEOUT"}
@@ -55,6 +60,15 @@ SIGNATURES = {
     "lsa_msa_attn_workspace_size": (_SZ, [_I64, _I64, _I32]),
     "lsa_msa_attn": (_I32, [_P, _P, _I64, _P, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _F32, _P, _P, _P, _SZ, _P]),
     "lsa_sparse_attn": (_I32, [_P, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _F32, _P, _P, _P, _SZ, _P]),
+    "lsa_rope_freqs": (_I32, [_I32, ctypes.c_double, _I32, ctypes.c_double, _I64, ctypes.c_double, ctypes.c_double, _P,
+                              _P]),
+    "lsa_norm_rope": (_I32, [_P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _P, _F32, _P, _I32, _I32, _I32, _F32, _P, _P,
+                             _I64, _I64, _I32, _P, _P]),
+    "lsa_cache_append": (_I32, [_P, _I64, _I64, _I32, _I32, _P, _F32, _P, _I32, _F32, _P, _P, _P, _I64, _P, _I64, _I32,
+                                _I32, _P, _P, _F32, _I32, _I32, _P, _I32, _P, _P]),
+    "lsa_prefix_attn": (_I32, [_P, _I64, _I32, _I32, _I32, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _F32, _P, _P, _P,
+                               _SZ, _P]),
+    "lsa_prefix_attn_workspace_size": (_SZ, [_I64, _I32]),
     "lsa_workspace_size": (_SZ, [_I32, _I64, _I64, _I32, _I32, _I32, _I32]),
     "lsa_device_status": (_I32, [_P]),
     "lsa_selftest_wait": (_I32, [ctypes.c_uint64, _P]),
@@ -295,6 +309,143 @@ def lsa_msa_attn(q, kv, idx, gmask, count, G, scale, out, lse=None, ws=None, str
                                      _ptr(count), B, H, d_qk, d_v, G, float(scale), _ptr(out), _ptr(lse), _ptr(ws),
                                      0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
     _check("lsa_msa_attn", st)
+
+
+def _need(fn: str, ok: bool, what: str):
+    if not ok:
+        raise LsaError(fn, -1, what)
+
+
+def _vec(fn: str, name: str, t, dtype, shape, device):
+    """Address of an optional contiguous tensor of this dtype, shape and device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise LsaError(fn, -1, f"{name}: contiguous {dtype} {tuple(shape)} on {device} wanted, got {t.dtype} "
+                               f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _code(fn: str, name: str, table: dict, key) -> int:
+    if key not in table:
+        raise LsaError(fn, -1, f"{name} must be one of {', '.join(table)}, got {key!r}")
+    return table[key]
+
+
+_same_device = contextlib.nullcontext()
+
+
+def _on(t):
+    """The tensors' GPU as the current one for the call (its stream, its kernels)."""
+    return _same_device if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _strides(fn: str, name: str, t):
+    """Token and head strides of [T, H, D] in elements; an axis of length one has none that matters."""
+    st, sh, sd = t.stride()
+    _need(fn, sd == 1 or t.shape[2] == 1, f"{name}: the last axis must be contiguous")
+    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+
+
+def lsa_rope_freqs(R, base=10000.0, scaling="none", factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0,
+                   device="cuda"):
+    """Angular frequencies of the position rotation (fp64 [R / 2] on `device`) and the factor of cos and sin."""
+    freqs, mul = torch.empty(max(int(R) // 2, 1), dtype=torch.float64), ctypes.c_float(0.0)
+    st = load_library().lsa_rope_freqs(int(R), float(base), _code("lsa_rope_freqs", "scaling", _SCALINGS, scaling),
+                                       float(factor), int(original_len), float(beta_fast), float(beta_slow),
+                                       freqs.data_ptr(), ctypes.byref(mul))
+    _check("lsa_rope_freqs", st)
+    return freqs.to(device), mul.value
+
+
+def lsa_norm_rope(x, y, pos=None, freqs=None, norm="none", weight=None, bias=None, eps=1e-6, rope_off=0,
+                  layout="interleaved", mul=1.0, y_scale=None, stream=None):
+    """y[t, h] = norm of x[t, h] with dims [rope_off, rope_off + 2 len(freqs)) rotated by pos[t]; x bf16 [T, H, D] with
+    any token and head strides, y bf16 (it may be x) or, with y_scale [T, H], e4m3 codes."""
+    fn = "lsa_norm_rope"
+    _need(fn, x.dim() == 3 and x.is_cuda and x.dtype == torch.bfloat16, "x: bf16 [T, H, D] on a GPU wanted")
+    _need(fn, y.shape == x.shape and y.device == x.device, "y: the shape and device of x wanted")
+    T, H, D = x.shape
+    dtype, dev, f32 = _dtype_code(y), x.device, torch.float32
+    xt, xh = _strides(fn, "x", x)
+    yt, yh = _strides(fn, "y", y)
+    _need(fn, (T == 1 or yt) and (H == 1 or yh), "y: a broadcast output")
+    _need(fn, pos is None or freqs is not None, "pos without freqs")
+    _need(fn, freqs is None or pos is not None, "freqs without pos")
+    with _on(x):
+        st = load_library().lsa_norm_rope(
+            x.data_ptr(), xt, xh, T, H, D, _code(fn, "norm", _NORMS, norm),
+            _vec(fn, "weight", weight, f32, (D,), dev), _vec(fn, "bias", bias, f32, (D,), dev), eps,
+            None if freqs is None else _vec(fn, "freqs", freqs, torch.float64, freqs.shape[:1], dev), rope_off,
+            0 if freqs is None else 2 * freqs.shape[0], _code(fn, "layout", _LAYOUTS, layout), mul,
+            _vec(fn, "pos", pos, torch.int64, (T,), dev), y.data_ptr(), yt, yh, dtype,
+            _vec(fn, "y_scale", y_scale, f32, (T, H), dev), _stream(stream))
+    _check(fn, st)
+
+
+def _rows(fn: str, name: str, t, T, D, device):
+    ok = t.shape == (T, D) and t.dtype == torch.bfloat16 and t.device == device and t.stride(1) == 1
+    _need(fn, ok, f"{name}: bf16 [{T}, {D}] on {device} with contiguous rows wanted")
+    return t.stride(0) if T > 1 else 0
+
+
+def lsa_cache_append(a, kv, slot, pos=None, freqs=None, kv_weight=None, kv_eps=1e-6, layout="interleaved", mul=1.0,
+                     k=None, k_cache=None, k_scale=None, k_norm="none", k_weight=None, k_bias=None, k_eps=1e-6,
+                     k_rope_off=-1, k_layout="half", stream=None):
+    """kv[slot[t]] = a[t] with its first 512 dims RMS-normed (kv_weight given) and its last 64 rotated by pos[t]; with k,
+    the index keys normed, rotated and written to k_cache[slot[t]] too (bf16, or e4m3 codes with k_scale)."""
+    fn = "lsa_cache_append"
+    dev, f32, i64 = a.device, torch.float32, torch.int64
+    T = slot.shape[0]
+    _need(fn, a.is_cuda, "tensors on a GPU wanted")
+    a_ld = _rows(fn, "a", a, T, 576, dev)
+    n = kv.shape[0]
+    _need(fn, (freqs is None) == (pos is None), "freqs and pos belong together")
+    _need(fn, (k is None) == (k_cache is None), "k and k_cache belong together")
+    k_ld = d_I = k_dtype = 0
+    k_cache_p = None
+    if k is not None:
+        d_I, k_dtype = k.shape[1], _dtype_code(k_cache)
+        k_ld = _rows(fn, "k", k, T, d_I, dev)
+        k_cache_p = _vec(fn, "k_cache", k_cache, k_cache.dtype, (n, d_I), dev)
+    with _on(a):
+        st = load_library().lsa_cache_append(
+            a.data_ptr(), a_ld, T, a.shape[1], 512, _vec(fn, "kv_weight", kv_weight, f32, (512,), dev), kv_eps,
+            _vec(fn, "freqs", freqs, torch.float64, (32,), dev), _code(fn, "layout", _LAYOUTS, layout), mul,
+            _vec(fn, "pos", pos, i64, (T,), dev), _vec(fn, "slot", slot, i64, (T,), dev),
+            _vec(fn, "kv", kv, torch.bfloat16, (n, 576), dev), n, _ptr(k), k_ld, d_I, _code(fn, "k_norm", _NORMS, k_norm),
+            _vec(fn, "k_weight", k_weight, f32, (d_I,), dev), _vec(fn, "k_bias", k_bias, f32, (d_I,), dev), k_eps,
+            k_rope_off if k is not None else -1, _code(fn, "k_layout", _LAYOUTS, k_layout), k_cache_p, k_dtype,
+            _vec(fn, "k_scale", k_scale, f32, (n,), dev), _stream(stream))
+    _check(fn, st)
+
+
+def lsa_prefix_attn_workspace_size(B, H):
+    return load_library().lsa_prefix_attn_workspace_size(B, H)
+
+
+def lsa_prefix_attn(q, prefix, scale, out, lse=None, pages=None, table=None, own_len=None, ws=None, stream=None):
+    """out[b, h] = softmax over the rows of `prefix` (None: no prefix) and the query's own own_len[b] rows in `pages`
+    ([n_pages, page, 576], found through table [B, cols]) of scale q.k, times the rows' first 512 dims."""
+    fn = "lsa_prefix_attn"
+    _need(fn, q.dim() == 3 and q.is_cuda, "q: bf16 [B, H, 576] on a GPU wanted")
+    B, H, d_qk = q.shape
+    dev, bf, i32 = q.device, torch.bfloat16, torch.int32
+    d_v, Lp, n_pages, page, cols = out.shape[-1], 0, 0, 0, 0
+    if prefix is not None:
+        Lp = prefix.shape[0]
+    _need(fn, (own_len is None) == (pages is None) == (table is None), "pages, table and own_len belong together")
+    if own_len is not None:
+        _need(fn, pages.dim() == 3 and table.dim() == 2, "pages [n_pages, page, 576] and table [B, cols] wanted")
+        n_pages, page, cols = pages.shape[0], pages.shape[1], table.shape[1]
+    with _on(q):
+        st = load_library().lsa_prefix_attn(
+            _vec(fn, "q", q, bf, q.shape, dev), B, H, d_qk, d_v, _vec(fn, "prefix", prefix, bf, (Lp, d_qk), dev), Lp,
+            _vec(fn, "pages", pages, bf, (n_pages, page, d_qk), dev), n_pages, page,
+            _vec(fn, "table", table, i32, (B, cols), dev), cols, _vec(fn, "own_len", own_len, i32, (B,), dev), scale,
+            _vec(fn, "out", out, bf, (B, H, d_v), dev), _vec(fn, "lse", lse, torch.float32, (B, H), dev), _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _check(fn, st)
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:

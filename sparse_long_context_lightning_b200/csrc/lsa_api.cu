@@ -184,13 +184,16 @@ int lsa_device_status(void* stream) {
   const int ix = take_index_timeout(), at = take_attn_timeout(&at_check), rs = take_rescore_timeout();
   const int a2 = take_attn2_flags(&a2_check), stw = take_selftest_timeout(), sm_check = take_attn_simt_check();
   const int tt = take_tree_tc_timeout(), ma = take_msa_attn_flags(&ma_check);
-  if (ix < 0 || at < 0 || rs < 0 || a2 < 0 || stw < 0 || sm_check < 0 || tt < 0 || ma < 0)
+  int pa_check = 0;
+  const int pa = take_prefix_flags(&pa_check), ap_check = take_append_check();
+  if (ix < 0 || at < 0 || rs < 0 || a2 < 0 || stw < 0 || sm_check < 0 || tt < 0 || ma < 0 || pa < 0 || ap_check < 0)
     return cuda_status(cudaGetLastError());
-  if (ix || at || rs || a2 || stw || tt || ma) {
+  if (ix || at || rs || a2 || stw || tt || ma || pa) {
     char msg[256];
-    std::snprintf(msg, sizeof(msg), "bounded wait gave up in:%s%s%s%s%s%s%s", ix ? " k_index_score_tc" : "",
+    std::snprintf(msg, sizeof(msg), "bounded wait gave up in:%s%s%s%s%s%s%s%s", ix ? " k_index_score_tc" : "",
                   at ? " k_sparse_attn_tc" : "", rs ? " k_rescore_tc" : "", a2 ? " k_sparse_attn_2p" : "",
-                  stw ? " k_selftest_wait" : "", tt ? " k_tree_child_tc" : "", ma ? " k_msa_attn_rows" : "");
+                  stw ? " k_selftest_wait" : "", tt ? " k_tree_child_tc" : "", ma ? " k_msa_attn_rows" : "",
+                  pa ? " k_prefix_attn" : "");
     set_last_error(msg);
     return LSA_ERR_TIMEOUT;
   }
@@ -201,6 +204,14 @@ int lsa_device_status(void* stream) {
                   "blocks) in:%s%s%s%s",
                   a2_check ? " k_sparse_attn_2p" : "", at_check ? " k_sparse_attn_tc" : "",
                   sm_check ? " k_attn_simt" : "", ma_check ? " k_msa_attn_rows" : "");
+    set_last_error(msg);
+    return LSA_ERR_DEVICE_CHECK;
+  }
+  if (pa_check || ap_check) {
+    char msg[256];
+    std::snprintf(msg, sizeof(msg), "device check failed in:%s%s",
+                  pa_check ? " k_prefix_attn (own_len outside [0, table columns * page], or a bad page id)" : "",
+                  ap_check ? " k_cache_append (a slot outside [-1, n_slots); the row was skipped)" : "");
     set_last_error(msg);
     return LSA_ERR_DEVICE_CHECK;
   }
@@ -636,10 +647,105 @@ int lsa_sparse_attn(const void* q, const void* kv, int64_t L, const int32_t* idx
                             static_cast<cudaStream_t>(stream));
 }
 
+int lsa_rope_freqs(int R, double base, int scaling, double factor, int64_t original_len, double beta_fast,
+                   double beta_slow, double* freqs, float* mul) {
+  LSA_CHECK_ARG(R >= 2 && R <= 1024 && R % 2 == 0 && base > 1.0 && base < 1e300 && freqs && mul);
+  LSA_CHECK_ARG(scaling == LSA_ROPE_PLAIN || scaling == LSA_ROPE_LINEAR || scaling == LSA_ROPE_YARN);
+  if (scaling != LSA_ROPE_PLAIN) LSA_CHECK_ARG(factor >= 1.0 && factor < 1e300);
+  if (scaling == LSA_ROPE_YARN) LSA_CHECK_ARG(original_len >= 1 && beta_slow > 0.0 && beta_fast >= beta_slow);
+  rope_freqs(R, base, scaling, factor, original_len, beta_fast, beta_slow, freqs, mul);
+  return LSA_OK;
+}
+
+int lsa_norm_rope(const void* x, int64_t x_ldt, int64_t x_ldh, int64_t T, int H, int D, int norm, const float* weight,
+                  const float* bias, float eps, const double* freqs, int rope_off, int rope_dims, int layout, float mul,
+                  const int64_t* pos, void* y, int64_t y_ldt, int64_t y_ldh, int dtype, float* y_scale, void* stream) {
+  LSA_CHECK_ARG(T >= 0 && H >= 1 && H <= 65535 && D >= 1);
+  LSA_CHECK_ARG(norm == LSA_NORM_NONE || norm == LSA_NORM_RMS || norm == LSA_NORM_LAYER);
+  LSA_CHECK_ARG(norm != LSA_NORM_NONE || (weight == nullptr && bias == nullptr));
+  LSA_CHECK_ARG(bias == nullptr || norm == LSA_NORM_LAYER);
+  LSA_CHECK_ARG(norm == LSA_NORM_NONE || (eps >= 0.f && eps < 1e30f));
+  LSA_CHECK_ARG(dtype == LSA_BF16 || dtype == LSA_FP8_E4M3);
+  LSA_CHECK_ARG((dtype == LSA_FP8_E4M3) == (y_scale != nullptr));
+  if (D % 8 != 0 || D > 1024) return LSA_ERR_UNSUPPORTED;
+  if (freqs) {
+    LSA_CHECK_ARG(layout == LSA_ROPE_INTERLEAVED || layout == LSA_ROPE_HALF);
+    LSA_CHECK_ARG(rope_off >= 0 && rope_dims >= 2 && rope_off <= D - rope_dims);
+    if (rope_off % 8 != 0 || rope_dims % 16 != 0) return LSA_ERR_UNSUPPORTED;
+  }
+  if (T == 0) return LSA_OK;
+  LSA_CHECK_ARG(x && y && (freqs == nullptr || pos));
+  LSA_CHECK_ARG(aligned16(x) && (reinterpret_cast<uintptr_t>(y) & (dtype == LSA_BF16 ? 15u : 7u)) == 0);
+  LSA_CHECK_ARG(x_ldt % 8 == 0 && x_ldh % 8 == 0 && y_ldt % 8 == 0 && y_ldh % 8 == 0);
+  return launch_norm_rope(x, x_ldt, x_ldh, T, H, D, norm, weight, bias, eps, freqs, rope_off, rope_dims, layout, mul, pos,
+                          y, y_ldt, y_ldh, dtype, y_scale, static_cast<cudaStream_t>(stream));
+}
+
+int lsa_cache_append(const void* a, int64_t a_ld, int64_t T, int d_qk, int d_v, const float* kv_weight, float kv_eps,
+                     const double* freqs, int layout, float mul, const int64_t* pos, const int64_t* slot, void* kv,
+                     int64_t n_slots, const void* k, int64_t k_ld, int d_I, int k_norm, const float* k_weight,
+                     const float* k_bias, float k_eps, int k_rope_off, int k_layout, void* k_cache, int k_dtype,
+                     float* k_scale, void* stream) {
+  LSA_CHECK_ARG(T >= 0 && n_slots >= 0);
+  if (d_qk != 576 || d_v != 512) return LSA_ERR_UNSUPPORTED;
+  LSA_CHECK_ARG(kv_weight == nullptr || (kv_eps >= 0.f && kv_eps < 1e30f));
+  LSA_CHECK_ARG(freqs == nullptr || layout == LSA_ROPE_INTERLEAVED || layout == LSA_ROPE_HALF);
+  if (k) {
+    if (d_I != 32 && d_I != 64 && d_I != 128) return LSA_ERR_UNSUPPORTED;
+    LSA_CHECK_ARG(k_norm == LSA_NORM_NONE || k_norm == LSA_NORM_RMS || k_norm == LSA_NORM_LAYER);
+    LSA_CHECK_ARG(k_norm != LSA_NORM_NONE || (k_weight == nullptr && k_bias == nullptr));
+    LSA_CHECK_ARG(k_bias == nullptr || k_norm == LSA_NORM_LAYER);
+    LSA_CHECK_ARG(k_norm == LSA_NORM_NONE || (k_eps >= 0.f && k_eps < 1e30f));
+    LSA_CHECK_ARG(k_dtype == LSA_BF16 || k_dtype == LSA_FP8_E4M3);
+    LSA_CHECK_ARG((k_dtype == LSA_FP8_E4M3) == (k_scale != nullptr));
+    if (k_rope_off >= 0) {
+      LSA_CHECK_ARG(freqs && k_rope_off <= d_I - 64);
+      LSA_CHECK_ARG(k_layout == LSA_ROPE_INTERLEAVED || k_layout == LSA_ROPE_HALF);
+      if (k_rope_off % 8 != 0) return LSA_ERR_UNSUPPORTED;
+    }
+  } else {
+    LSA_CHECK_ARG(k_cache == nullptr && k_scale == nullptr && k_weight == nullptr && k_bias == nullptr);
+  }
+  if (T == 0) return LSA_OK;
+  LSA_CHECK_ARG(a && slot && kv && (freqs == nullptr || pos) && (k == nullptr || k_cache));
+  LSA_CHECK_ARG(aligned16(a) && aligned16(kv) && a_ld % 8 == 0);
+  LSA_CHECK_ARG(k == nullptr || (aligned16(k) && aligned16(k_cache) && k_ld % 8 == 0));
+  return launch_cache_append(a, a_ld, kv_weight, kv_eps, k, k_ld, d_I, k_norm, k_weight, k_bias, k_eps,
+                             k_rope_off < 0 ? -1 : k_rope_off, k_layout, freqs, layout, mul, pos, slot, T, kv, n_slots,
+                             k_cache, k_dtype, k_scale, static_cast<cudaStream_t>(stream));
+}
+
+size_t lsa_prefix_attn_workspace_size(int64_t B, int H) {
+  if (B < 0 || H < 1 || H > 65535 || B > 65535) return static_cast<size_t>(-1);
+  return prefix_attn_ws_bytes(B, H);
+}
+
+int lsa_prefix_attn(const void* q, int64_t B, int H, int d_qk, int d_v, const void* prefix, int64_t Lp,
+                    const void* pages, int64_t n_pages, int page, const int32_t* table, int64_t table_ld,
+                    const int32_t* own_len, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                    void* stream) {
+  LSA_CHECK_ARG(B >= 0 && H >= 1 && H <= 65535 && Lp >= 0 && n_pages >= 0 && table_ld >= 0);
+  LSA_CHECK_ARG(scale > -1e30f && scale < 1e30f);
+  if (d_qk != 576 || d_v != 512) return LSA_ERR_UNSUPPORTED;
+  if (own_len) {
+    LSA_CHECK_ARG(page >= 1);
+    if (page < 8 || page > 65536 || (page & (page - 1)) != 0) return LSA_ERR_UNSUPPORTED;
+    LSA_CHECK_ARG(table_ld < (int64_t(1) << 31));
+    // rows of a tile map are 32-bit
+    if (n_pages > (int64_t(0x7FFF0000) / page)) return LSA_ERR_UNSUPPORTED;
+  }
+  if (Lp > 0x7FFF0000 || B * H > 0x7FFF0000) return LSA_ERR_UNSUPPORTED;
+  if (B == 0) return LSA_OK;
+  LSA_CHECK_ARG(B <= 65535);
+  LSA_CHECK_ARG(q && out && (Lp == 0 || prefix));
+  LSA_CHECK_ARG(aligned16(q) && aligned16(out) && (Lp == 0 || aligned16(prefix)));
+  if (own_len) {
+    LSA_CHECK_ARG(table_ld == 0 || table);
+    LSA_CHECK_ARG(n_pages == 0 || (pages && aligned16(pages)));
+  }
+  if (ws == nullptr || !aligned256(ws) || ws_bytes < prefix_attn_ws_bytes(B, H)) return LSA_ERR_WORKSPACE;
+  return launch_prefix_attn(q, B, H, prefix, Lp, pages, own_len ? n_pages : 0, own_len ? page : 8, table,
+                            own_len ? table_ld : 0, own_len, scale, out, lse, ws, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"
-
-namespace lsa {
-
-
-
-}  // namespace lsa

@@ -195,4 +195,21 @@ int take_attn2_flags(int* check);
 int take_msa_attn_flags(int* check);
 int launch_msa_attn_rows(const void* q, const void* kv, int64_t L, const int32_t* idx, const uint8_t* gmask, int64_t ld,
                          const int32_t* count, int64_t B, int G, float scale, void* out, float* lse, cudaStream_t s);
+int launch_norm_rope(const void* x, int64_t ldt, int64_t ldh, int64_t T, int H, int D, int norm, const float* weight,
+                     const float* bias, float eps, const double* freqs, int off, int R, int layout, float mul,
+                     const int64_t* pos, void* y, int64_t yldt, int64_t yldh, int dtype, float* scale,
+                     cudaStream_t s);
+int launch_cache_append(const void* x, int64_t ldx, const float* x_weight, float x_eps, const void* k, int64_t ldk,
+                        int d_I, int k_norm, const float* k_weight, const float* k_bias, float k_eps, int k_off,
+                        int k_layout, const double* freqs, int layout, float mul, const int64_t* pos,
+                        const int64_t* slot, int64_t T, void* kv, int64_t n_slots, void* kc, int k_dtype,
+                        float* k_scale, cudaStream_t s);
+void rope_freqs(int R, double base, int scaling, double factor, int64_t original_len, double beta_fast,
+                double beta_slow, double* freqs, float* mul);
+int take_append_check();
+size_t prefix_attn_ws_bytes(int64_t B, int H);
+int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int64_t Lp, const void* pages,
+                       int64_t n_pages, int page, const int32_t* table, int64_t table_ld, const int32_t* own_len,
+                       float scale, void* out, float* lse, void* ws, cudaStream_t s);
+int take_prefix_flags(int* check);
 }  // namespace lsa
