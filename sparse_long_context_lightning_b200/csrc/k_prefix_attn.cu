@@ -3,152 +3,693 @@
 //   o = sum_k e^{scale q.k - m} v_k / l,  l = sum_k e^{scale q.k - m},  lse = m + ln l,  v = the first 512 dims of k,
 // over the Lp rows of the prefix (the same for every query) and own_len[b] rows behind them (block table).
 //
-// One block a query and eight of its heads, a warp a head: tiles of 32 keys in shared memory serve the eight heads,
-// a lane forms one key's logit, and a lane holds 16 of the 512 output dims.  CUDA cores, so 2 (576 + 512) flops a
-// (head, key) bound it, and every block reads the whole prefix.
+// The batch's B * H query rows are cut into tiles of 128, whatever H is, and every tile walks the prefix in blocks of
+// 64 keys, then the blocks of its own queries' pages, with one running maximum and sum per row.  2 (576 + 512) flops a
+// (row, key) against 1152 bytes a key: from about 190 rows on the matrix units bound it, below that the prefix's bytes.
+//
+// A CTA pair (cluster of two, tcgen05 cta_group::2, M = 128) takes a tile: each CTA has 64 rows of Q, their logits,
+// probabilities and output, so the softmax never leaves the CTA, and feeds half of every B operand: 32 of a block's 64
+// keys for S = Q K^T (N = 64) and 256 of the 512 value dims for O += P V (two N = 256 instructions a 16 keys).  A
+// 128 x 512 fp32 output would fill a CTA's tensor memory; the pair's 64 rows a CTA take half of it and leave room for
+// four buffers of S, so the logits run ahead of the softmax.  The same bytes cannot serve as keys and as values here
+// (one descriptor gives both CTAs' halves of B, and the halves are cut along different axes), so a block is loaded
+// twice, 1088 bytes a key and CTA, the second time from L2: this loop without its softmax, fed from L2, ran at 1440 to
+// 1545 TFLOP/s, the same matrix instructions without loads at 1531, the loads alone at 20 TB/s.
+// N = 64 costs 22.6 clocks a key and SM against 17.0 at N = 128 (A is read again for every block), but two stages of
+// 128 keys do not fit beside Q; 96 keys in one stage each ran at 1080 to 1150.
+//
+// Work is cut evenly: the blocks of all tiles, in order, are one line that 74 pairs divide; a tile that spans pairs
+// leaves partial sums (fp32) that k_prefix_combine joins.  Where a tile holds several queries (H not a multiple of 128),
+// each query's own blocks are an accumulation of their own, so that a row never multiplies another sequence's values.
 #include "lsa_common.cuh"
-#include "sm100.cuh"
+#include "sm100_pair.cuh"
 
 namespace lsa {
 namespace {
 
-__device__ int g_prefix_check;  // set when own_len was outside [0, the table's columns * page] or a page id was bad
+using namespace sm100;
+
+__device__ int g_prefix_timeout;  // set when a bounded wait gave up
+__device__ int g_prefix_check;    // set when own_len was outside [0, the table's columns * page] or a page id was bad
 
 constexpr int PA_THREADS = 256;
-constexpr int PA_T = 32;        // keys of a tile
-constexpr int PA_LD = 576 + 8;  // bf16 elements of a tile's row: 16-byte reads of 8 rows meet every bank once
-constexpr int PA_SMEM = 8 * 576 * 4 + PA_T * PA_LD * 2;
+constexpr int PA_KQ_WARP = 0, PA_QK_WARP = 1, PA_PV_WARP = 2, PA_V_WARP = 3, PA_SM_WARP = 4;
+constexpr int PA_PAIRS = 74;  // one pair on every two of the 148 SMs
+constexpr int PA_T = 64;      // keys of a block
+constexpr int PA_ROWS = 128;  // query rows of a tile
+constexpr int PA_NK = 2, PA_NV = 2, PA_NS = 4, PA_NP = 2;
+constexpr int PA_Q_KB = 64 * 128;         // 64 rows x 64 dims
+constexpr int PA_Q_BYTES = 9 * PA_Q_KB;   // 72 KB
+constexpr int PA_P_BYTES = 64 * 128;      // 64 rows x 64 keys
+constexpr int PA_K_KB = PA_T / 2 * 128;   // 32 keys x 64 dims
+constexpr int PA_K_BYTES = 9 * PA_K_KB;   // 36 KB
+constexpr int PA_V_KB = PA_T * 128;       // 64 keys x 64 dims
+constexpr int PA_V_BYTES = 4 * PA_V_KB;   // 32 KB
+constexpr int PA_SMEM = 1024 + PA_Q_BYTES + PA_NP * PA_P_BYTES + PA_NK * PA_K_BYTES + PA_NV * PA_V_BYTES + 3 * 512 + 512;
+static_assert(PA_SMEM <= 232448, "shared memory");
+constexpr uint32_t PT_O = 0, PT_S = 256;  // TMEM columns: O [0, 256), S buffers of 32 from 256
+constexpr uint32_t IDESC_QK = idesc_mma(128, PA_T, 1u, 0u);
+constexpr uint32_t IDESC_PV2 = idesc_mma(128, 256, 1u, 1u);
+constexpr float PA_RESCALE = 8.f;
+constexpr int PA_NO_ROW = 0x7FFFFF00;  // behind every map's last row: the box reads as zeros
 
 struct PaArgs {
-  const uint16_t* q;
-  const uint16_t* prefix;
-  const uint16_t* pages;
   const int32_t* own_len;  // [B], or NULL: no own tokens
   const int32_t* table;    // [B, table_ld] page ids
   int64_t table_ld;
-  int page_shift;
-  int64_t n_pages;
-  int64_t cap;  // most own tokens
+  int page_shift;  // log2 of the page size
+  int box;         // rows of a page box: min(page, 32)
+  int n_pages;
+  int cap;  // most own tokens: the table's columns * page (clamped to int)
+  int B, H;
+  int64_t BH;
+  int nT;     // tiles
+  int multi;  // tiles may hold rows of several queries
   int64_t Lp;
-  int H;
-  float scale;
+  int nP;  // prefix blocks
+  float scale_log2;
+  int2* seg;      // [items] first and last pair of an item
+  float2* ws_ml;  // [slots][128] running max (log2 units), sum
+  float* ws_o;    // [slots][128][512]
 };
 
-__global__ void __launch_bounds__(PA_THREADS) k_prefix_attn(const PaArgs a, uint16_t* __restrict__ out,
-                                                            float* __restrict__ lse) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  float* q_s = reinterpret_cast<float*>(smem);
-  uint16_t* k_s = reinterpret_cast<uint16_t*>(smem + 8 * 576 * 4);
-  sm100::pdl_wait();
-  sm100::pdl_launch_dependents();
-  const int groups = (a.H + 7) / 8;
-  const int64_t b = blockIdx.x / groups;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h0 = static_cast<int>(blockIdx.x % groups) * 8, h = h0 + warp;
-  for (int i = threadIdx.x; i < 8 * 576; i += PA_THREADS)
-    q_s[i] = h0 + i / 576 < a.H ? bf16_bits_to_f32(a.q[(b * a.H + h0) * 576 + i]) : 0.f;
-  int64_t own = a.own_len ? a.own_len[b] : 0;
-  if (own < 0 || own > a.cap) {
-    if (threadIdx.x == 0) atomicExch(&g_prefix_check, 1);
-    own = own < 0 ? 0 : a.cap;
+// Items: a tile where all rows belong to one query; else a tile's prefix part, and each of its queries' own part.
+// Their numbers rise along the line of blocks, and so does number + pair: the slot of a (item, pair) partial.
+struct Cursor {
+  int t, b;  // tile; query whose own blocks are walked, or -1: the prefix
+  int pos, cnt;
+  int qlo, qhi;
+
+  static __device__ __forceinline__ int len_of(const PaArgs& a, int b) {
+    if (a.own_len == nullptr) return 0;
+    return min(max(__ldg(a.own_len + b), 0), a.cap);
   }
-  const int64_t n = a.Lp + own;
-  float m = -INFINITY, l = 0.f, o[16];
-  #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  for (int64_t k0 = 0; k0 < n; k0 += PA_T) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < PA_T * 72; i += PA_THREADS) {
-      const int64_t key = k0 + i / 72;
-      const uint16_t* row = nullptr;
-      if (key < a.Lp) {
-        row = a.prefix + key * 576;
-      } else if (key < n) {
-        const int64_t t = key - a.Lp;
-        const int32_t pg = a.table[b * a.table_ld + (t >> a.page_shift)];
-        if (pg >= 0 && pg < a.n_pages)
-          row = a.pages + ((static_cast<int64_t>(pg) << a.page_shift) + (t & ((1 << a.page_shift) - 1))) * 576;
-        else
-          atomicExch(&g_prefix_check, 1);
-      }
-      *reinterpret_cast<uint4*>(k_s + (i / 72) * PA_LD + (i % 72) * 8) =
-          row ? reinterpret_cast<const uint4*>(row)[i % 72] : make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    float z = 0.f;
-    for (int c = 0; c < 72; ++c) {
-      const uint4 v = *reinterpret_cast<const uint4*>(k_s + lane * PA_LD + c * 8);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z = fmaf(q_s[warp * 576 + c * 8 + 2 * i], __uint_as_float(u[i] << 16), z);
-        z = fmaf(q_s[warp * 576 + c * 8 + 2 * i + 1], __uint_as_float(u[i] & 0xFFFF0000u), z);
+  static __device__ __forceinline__ int blocks_of(const PaArgs& a, int b) { return (len_of(a, b) + PA_T - 1) / PA_T; }
+  __device__ __forceinline__ void tile(const PaArgs& a, int tt) {
+    t = tt;
+    b = -1;
+    cnt = a.nP;
+    const int64_t r0 = static_cast<int64_t>(tt) * PA_ROWS;
+    qlo = static_cast<int>(r0 / a.H);
+    qhi = static_cast<int>(min(r0 + PA_ROWS, a.BH) - 1) / a.H;
+  }
+  __device__ __forceinline__ void settle(const PaArgs& a) {  // to the block that `pos` counts up to; one must be left
+    while (pos >= cnt) {
+      pos -= cnt;
+      b = b < 0 ? qlo : b + 1;
+      if (b <= qhi) {
+        cnt = blocks_of(a, b);
+      } else if (t + 1 < a.nT) {
+        tile(a, t + 1);
+      } else {  // not reached unless own_len changed since the blocks were counted: rows outside the maps, zeros
+        b = -1;
+        cnt = 0x7FFFFFFF;
       }
     }
-    z = k0 + lane < n ? z * a.scale : -INFINITY;
-    const float mn = fmaxf(m, warp_max(z));
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float alpha = expf(m - ref), p = expf(z - ref);
-    l = l * alpha + warp_sum(p);
-    m = mn;
+  }
+  __device__ __forceinline__ void start(const PaArgs& a, int tt, int off) {
+    tile(a, tt);
+    pos = off;
+    settle(a);
+  }
+  __device__ __forceinline__ int id(const PaArgs& a) const {
+    return !a.multi ? t : (b < 0 ? qlo + 2 * t : b + 2 * t + 1);
+  }
+  __device__ __forceinline__ int item_pos(const PaArgs& a) const { return a.multi || b < 0 ? pos : a.nP + pos; }
+  __device__ __forceinline__ int item_cnt(const PaArgs& a) const { return a.multi ? cnt : a.nP + blocks_of(a, qlo); }
+};
+
+__device__ __forceinline__ int tile_blocks(const PaArgs& a, int t) {
+  Cursor c;
+  c.tile(a, t);
+  int n = a.nP;
+  if (a.own_len)
+    for (int b = c.qlo; b <= c.qhi; ++b) n += Cursor::blocks_of(a, b);
+  return n;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
+    k_prefix_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_p, const PaArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* q_s = base;
+  unsigned char* p_s = q_s + PA_Q_BYTES;
+  unsigned char* k_s = p_s + PA_NP * PA_P_BYTES;
+  unsigned char* v_s = k_s + PA_NK * PA_K_BYTES;
+  float* mx = reinterpret_cast<float*>(v_s + PA_NV * PA_V_BYTES);  // [3][128]: row maxima of two blocks, row sums
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(mx + 3 * 128);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_empty + 1;
+  uint64_t* k_empty = k_full + PA_NK;
+  uint64_t* v_full = k_empty + PA_NK;
+  uint64_t* v_empty = v_full + PA_NV;
+  uint64_t* s_full = v_empty + PA_NV;
+  uint64_t* s_empty = s_full + PA_NS;
+  uint64_t* p_full = s_empty + PA_NS;
+  uint64_t* pv_done = p_full + PA_NP;
+  uint64_t* vt_full = pv_done + PA_NP;  // this CTA's values of a block whose last page is partly filled
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(vt_full + 1);
+  int* start_s = reinterpret_cast<int*>(tmem_holder + 1);  // this pair's first tile, block of it, number of blocks
+  int* abort_flag = start_s + 3;
+
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < PA_NK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < PA_NV; ++i) {
+      mbar_init(&v_full[i], 2);  // one arrival a CTA
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < PA_NS; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 8);  // the softmax warps of both CTAs
+    }
+    for (int i = 0; i < PA_NP; ++i) {
+      mbar_init(&p_full[i], 8);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(vt_full, 1);
+    start_s[2] = 0;
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == PA_PV_WARP) tmem_alloc_pair(tmem_holder, 512);
+  // every global access of this kernel comes after the previous kernel of the stream has completed
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this pair's part of the line of blocks: thread i sums the tiles [i * per, (i + 1) * per), a scan over the
+  // threads, and the thread that holds the first block finds its tile
+  {
+    int64_t* sums = reinterpret_cast<int64_t*>(mx);
+    const int per = (a.nT + PA_THREADS - 1) / PA_THREADS;
+    const int lo = min(tid * per, a.nT), hi = min(lo + per, a.nT);
+    int64_t mine = 0;
+    for (int t = lo; t < hi; ++t) mine += tile_blocks(a, t);
+    int64_t inc = mine;
     #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] *= alpha;
-    const int keys = static_cast<int>(n - k0 < PA_T ? n - k0 : PA_T);
-    for (int k = 0; k < keys; ++k) {
-      const float pk = __shfl_sync(0xffffffffu, p, k);
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(k_s + k * PA_LD + 64 * i + 2 * lane);
-        o[2 * i] = fmaf(pk, __uint_as_float(v << 16), o[2 * i]);
-        o[2 * i + 1] = fmaf(pk, __uint_as_float(v & 0xFFFF0000u), o[2 * i + 1]);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - mine, total = 0;
+    for (int w = 0; w < PA_THREADS / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    const int64_t np = min(static_cast<int64_t>(PA_PAIRS), total);
+    if (pair < np) {
+      const int64_t s0 = total * pair / np, s1 = total * (pair + 1) / np;
+      if (s0 >= before && s0 < before + mine) {
+        int64_t off = s0 - before;
+        int t = lo;
+        for (int n = tile_blocks(a, t); off >= n && t + 1 < hi; n = tile_blocks(a, t)) {
+          off -= n;
+          ++t;
+        }
+        start_s[0] = t;
+        start_s[1] = static_cast<int>(off);
+        start_s[2] = static_cast<int>(s1 - s0);
       }
     }
+    if (blockIdx.x == 0 && a.own_len)
+      for (int b = tid; b < a.B; b += PA_THREADS)
+        if (a.own_len[b] < 0 || a.own_len[b] > a.cap) atomicExch(&g_prefix_check, 1);
   }
-  if (h >= a.H) return;
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the barriers and the tensor memory of both CTAs are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int n = start_s[2];
+  Cursor c;
+  if (n > 0) c.start(a, start_s[0], start_s[1]);
+  bool ok = true;
+
+  if (warp == PA_KQ_WARP) {
+    // ------------------------------------------------------------------ Q and keys
+    int loaded = -1, nq = 0;
+    for (int i = 0; i < n && ok; ++i) {
+      // page rows of this CTA's 32 keys (lane = box); a box past the end reads as zeros: a row outside the map
+      int y = 0;
+      if (c.b >= 0) {
+        const int key = PA_T * c.pos + 32 * static_cast<int>(rank) + lane * a.box;
+        y = PA_NO_ROW;
+        if (lane * a.box < 32 && key < Cursor::len_of(a, c.b)) {
+          const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
+          if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+        }
+      }
+      if (c.t != loaded) {
+        ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1));
+        if (ok && elect_one()) {
+          if (rank == 0) mbar_expect_tx(q_full, 2 * PA_Q_BYTES);
+          const uint32_t bar = mapa(smem_u32(q_full), 0);
+          for (int j = 0; j < 9; ++j)
+            tma_load_2d_pair(q_s + j * PA_Q_KB, &tm_q, bar, 64 * j, c.t * PA_ROWS + 64 * static_cast<int>(rank));
+        }
+        __syncwarp();
+        loaded = c.t;
+        ++nq;
+      }
+      const int s = i % PA_NK;
+      ok = ok && mbar_spin(&k_empty[s], ((i / PA_NK) & 1) ^ 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const uint32_t bar = mapa(smem_u32(&k_full[s]), 0);
+      unsigned char* dst = k_s + s * PA_K_BYTES;
+      const bool one = elect_one();
+      if (one && rank == 0) mbar_expect_tx(&k_full[s], 2 * PA_K_BYTES);
+      if (c.b < 0) {
+        if (one)
+          for (int j = 0; j < 9; ++j)
+            tma_load_2d_pair(dst + j * PA_K_KB, &tm_k, bar, 64 * j, PA_T * c.pos + 32 * static_cast<int>(rank));
+      } else {
+        for (int r = 0; r * a.box < 32; ++r) {
+          const int yr = __shfl_sync(0xffffffffu, y, r);
+          if (one)
+            for (int j = 0; j < 9; ++j)
+              tma_load_2d_pair(dst + j * PA_K_KB + r * a.box * 128, &tm_p, bar, 64 * j, yr);
+        }
+      }
+      __syncwarp();
+      ++c.pos;
+      if (i + 1 < n) c.settle(a);
+    }
+  } else if (warp == PA_V_WARP) {
+    // ------------------------------------------------------------------ values: this CTA's 256 dims of all 64 keys
+    int ntail = 0;
+    for (int i = 0; i < n && ok; ++i) {
+      int y = 0, valid = PA_T;
+      if (c.b >= 0) {
+        const int len = Cursor::len_of(a, c.b), key = PA_T * c.pos + lane * a.box;
+        valid = min(PA_T, len - PA_T * c.pos);
+        y = PA_NO_ROW;
+        if (lane * a.box < PA_T && key < len) {
+          const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
+          if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+          else atomicExch(&g_prefix_check, 1);
+        }
+      }
+      const int s = i % PA_NV;
+      ok = mbar_spin(&v_empty[s], ((i / PA_NV) & 1) ^ 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      unsigned char* dst = v_s + s * PA_V_BYTES;
+      const bool one = elect_one();
+      if (c.b < 0) {
+        if (one) {
+          if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
+          else mbar_arrive_cluster(mapa(smem_u32(&v_full[s]), 0));
+          const uint32_t bar = mapa(smem_u32(&v_full[s]), 0);
+          for (int j = 0; j < 4; ++j)
+            tma_load_2d_pair(dst + j * PA_V_KB, &tm_v, bar, 256 * static_cast<int>(rank) + 64 * j, PA_T * c.pos);
+        }
+      } else {
+        // rows of a partly filled box behind the sequence's end hold anything (NaN too) and would meet p = 0 in the
+        // product: such a block lands on this CTA's own barrier, has those rows zeroed, and is then handed over
+        const bool tail = (valid & (a.box - 1)) != 0;
+        const uint32_t bar = tail ? mapa(smem_u32(vt_full), rank) : mapa(smem_u32(&v_full[s]), 0);
+        if (one) {
+          if (tail) mbar_expect_tx(vt_full, PA_V_BYTES);
+          else if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
+          else mbar_arrive_cluster(mapa(smem_u32(&v_full[s]), 0));
+        }
+        __syncwarp();
+        for (int r = 0; r * a.box < PA_T; ++r) {
+          const int yr = __shfl_sync(0xffffffffu, y, r);
+          if (one)
+            for (int j = 0; j < 4; ++j)
+              tma_load_2d_pair(dst + j * PA_V_KB + r * a.box * 128, &tm_p, bar, 256 * static_cast<int>(rank) + 64 * j, yr);
+        }
+        if (tail) {
+          ok = mbar_wait(vt_full, ntail & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          ++ntail;
+          const int rows = min(PA_T, (valid + a.box - 1) / a.box * a.box) - valid;
+          for (int x = lane; x < 4 * rows * 8; x += 32) {
+            const int j = x / (rows * 8), e = x - j * rows * 8;
+            *reinterpret_cast<uint4*>(dst + j * PA_V_KB + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (one) mbar_arrive_cluster(mapa(smem_u32(&v_full[s]), 0));
+        }
+      }
+      __syncwarp();
+      ++c.pos;
+      if (i + 1 < n) c.settle(a);
+    }
+  } else if (warp == PA_QK_WARP) {
+    // ------------------------------------------------------------------ S = Q K^T (issued by the even CTA)
+    if (rank == 0 && n > 0 && elect_one()) {
+      const uint64_t qdesc = desc_sw128(smem_u32(q_s));
+      int nq = 0;
+      bool fresh = true;
+      for (int i = 0; i < n; ++i) {
+        const int s = i % PA_NK, sb = i % PA_NS;
+        if (fresh) ok = mbar_wait_cluster(q_full, nq++ & 1);
+        ok = ok && mbar_wait_cluster(&s_empty[sb], ((i / PA_NS) & 1) ^ 1) && mbar_wait_cluster(&k_full[s], (i / PA_NK) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kdesc = desc_sw128(smem_u32(k_s + s * PA_K_BYTES));
+        #pragma unroll
+        for (int kb = 0; kb < 9; ++kb) {
+          #pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_pair(tmem + PT_S + sb * (PA_T / 2), qdesc + ((kb * PA_Q_KB + kk * 32) >> 4),
+                         kdesc + ((kb * PA_K_KB + kk * 32) >> 4), IDESC_QK, (kb | kk) != 0);
+        }
+        mma_commit_pair(&k_empty[s]);
+        mma_commit_pair(&s_full[sb]);
+        const int t = c.t;
+        ++c.pos;
+        if (i + 1 < n) c.settle(a);
+        fresh = c.t != t;
+        if (fresh) mma_commit_pair(q_empty);
+      }
+    }
+  } else if (warp == PA_PV_WARP) {
+    // ------------------------------------------------------------------ O += P V (issued by the even CTA)
+    if (rank == 0 && n > 0 && elect_one()) {
+      int item = -1;
+      for (int i = 0; i < n; ++i) {
+        const int s = i % PA_NV, pb = i % PA_NP;
+        ok = mbar_wait_cluster(&v_full[s], (i / PA_NV) & 1) && mbar_wait_cluster(&p_full[pb], (i / PA_NP) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t first = c.id(a) != item;
+        item = c.id(a);
+        const uint64_t pdesc = desc_sw128(smem_u32(p_s + pb * PA_P_BYTES));
+        const uint32_t v_addr = smem_u32(v_s + s * PA_V_BYTES);
+        #pragma unroll
+        for (int kk = 0; kk < PA_T / 16; ++kk) {
+          #pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma_f16_pair(tmem + PT_O + h * 128, pdesc + ((kk * 32) >> 4),
+                         desc_sw128_mn(v_addr + 2 * h * PA_V_KB + kk * 16 * 128, PA_V_KB, 1024), IDESC_PV2,
+                         kk > 0 || !first);
+        }
+        mma_commit_pair(&v_empty[s]);
+        mma_commit_pair(&pv_done[pb]);
+        ++c.pos;
+        if (i + 1 < n) c.settle(a);
+      }
+    }
+  } else if (n > 0) {
+    // ------------------------------------------------------------------ softmax and partial sums
+    // Thread L: row L % 64 of this CTA, keys [32 (L / 64), 32 (L / 64) + 32) of a block, value dims
+    // [256 (L / 64), 256 (L / 64) + 256).  A wait that gave up is not waited for again, but the loop goes on: the
+    // four warps meet at a named barrier in every block.
+    const int L = (warp - PA_SM_WARP) * 32 + lane;
+    const int row = L & 63, kh = L >> 6;
+    const int trow = 64 * static_cast<int>(rank) + row;  // row of the tile
+    const uint32_t tlane = tmem + (static_cast<uint32_t>((warp - PA_SM_WARP) * 32) << 16);
+    const uint32_t c_s_empty = mapa(smem_u32(s_empty), 0), c_p_full = mapa(smem_u32(p_full), 0);
+    float m_used = -INFINITY, l = 0.f;
+    bool first = true;
+    int seg_pos = c.item_pos(a);
+    for (int i = 0; i < n; ++i) {
+      const int sb = i % PA_NS, pb = i % PA_NP;
+      // keys of this thread that exist, and whether its row may see them
+      int nvalid;
+      if (c.b < 0) {
+        nvalid = static_cast<int>(min(static_cast<int64_t>(PA_T), a.Lp - static_cast<int64_t>(PA_T) * c.pos));
+      } else {
+        nvalid = min(PA_T, Cursor::len_of(a, c.b) - PA_T * c.pos);
+        const int64_t gr = static_cast<int64_t>(c.t) * PA_ROWS + trow;
+        if (a.multi && (gr < static_cast<int64_t>(c.b) * a.H || gr >= static_cast<int64_t>(c.b + 1) * a.H)) nvalid = 0;
+      }
+      nvalid -= 32 * kh;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&s_full[sb], (i / PA_NS) & 1));
+      tc_fence_after();
+      uint32_t sr[32];
+      tmem_ld32(tlane + PT_S + sb * (PA_T / 2), sr);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(c_s_empty + 8 * sb);
+      float z[32];
+      #pragma unroll
+      for (int k = 0; k < 32; ++k) z[k] = k < nvalid ? __uint_as_float(sr[k]) * a.scale_log2 : -INFINITY;
+      float m4[4] = {z[0], z[1], z[2], z[3]};
+      #pragma unroll
+      for (int k = 4; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], z[k]);
+      float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      // the row's other 32 keys are another warp's
+      mx[128 * (i & 1) + L] = mt;
+      named_bar_sync(1, 128);
+      mt = fmaxf(mt, mx[128 * (i & 1) + (L ^ 64)]);
+      float alpha = 1.f;
+      if (mt > m_used + PA_RESCALE || (first && mt > m_used)) {
+        alpha = ex2_approx(m_used - mt);  // 0 from -inf
+        m_used = mt;
+      }
+      const float m_ref = m_used == -INFINITY ? 0.f : m_used;
+      uint32_t pk[16];
+      float s4[4] = {0.f, 0.f, 0.f, 0.f};
+      #pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        const float p0 = ex2_approx(z[k] - m_ref), p1 = ex2_approx(z[k + 1] - m_ref);
+        // the row's sum takes the 32-bit probabilities; P V takes them rounded to bf16 (the matrix unit's type)
+        s4[(k >> 1) & 3] += p0 + p1;
+        const __nv_bfloat162 p2 = __floats2bfloat162_rn(p0, p1);
+        pk[k / 2] = *reinterpret_cast<const uint32_t*>(&p2);
+      }
+      l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+      if (i >= PA_NP && ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i / PA_NP) - 1) & 1));
+      // O changes its reference only when a maximum grew by more than 2^8 (no product is running then)
+      if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[(i - 1) % PA_NP], ((i - 1) / PA_NP) & 1));
+        tc_fence_after();
+        #pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          uint32_t o[32];
+          tmem_ld32(tlane + PT_O + 32 * k, o);
+          tmem_ld_wait();
+          #pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(tlane + PT_O + 32 * k, o);
+        }
+        tmem_st_wait();
+      }
+      unsigned char* prow = p_s + pb * PA_P_BYTES + row * 128;
+      #pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(prow + (((4 * kh + e) ^ (row & 7)) << 4)) =
+            make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(c_p_full + 8 * pb);
+      first = false;
+
+      const int id = c.id(a), tile = c.t, own = c.b, ipos = c.item_pos(a), icnt = c.item_cnt(a);
+      ++c.pos;
+      if (i + 1 < n) c.settle(a);
+      if (i + 1 < n && c.id(a) == id) continue;
+      // ---- the item's (or this pair's) last block: the partial sums of its rows
+      mx[256 + L] = l;
+      named_bar_sync(1, 128);
+      const float lt = l + mx[256 + (L ^ 64)];
+      if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], (i / PA_NP) & 1));
+      tc_fence_after();
+      const int64_t gr = static_cast<int64_t>(tile) * PA_ROWS + trow;
+      const bool live = gr < a.BH && (!a.multi || own < 0 || (gr >= static_cast<int64_t>(own) * a.H &&
+                                                               gr < static_cast<int64_t>(own + 1) * a.H));
+      const int64_t prow_i = static_cast<int64_t>(id + pair) * PA_ROWS + trow;
+      #pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        uint32_t o[32];
+        tmem_ld32(tlane + PT_O + 32 * k, o);
+        tmem_ld_wait();
+        if (live) {
+          uint4* d = reinterpret_cast<uint4*>(a.ws_o + prow_i * 512 + 256 * kh + 32 * k);
+          #pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      tc_fence_before();
+      if (live && kh == 0) a.ws_ml[prow_i] = make_float2(m_used, lt);
+      if (rank == 0 && L == 0) {
+        if (seg_pos == 0) a.seg[id].x = pair;
+        if (ipos == icnt - 1) a.seg[id].y = pair;
+      }
+      m_used = -INFINITY;
+      l = 0.f;
+      first = true;
+      if (i + 1 < n) seg_pos = c.item_pos(a);
+    }
+  }
+  if (!ok) {
+    atomicExch(&g_prefix_timeout, 1);
+    *abort_flag = 1;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {  // copies and products that are still in flight end within microseconds
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  cluster_sync_all();  // the other CTA's products and arrivals end here too
+  if (warp == PA_PV_WARP) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// One block a row (b, h): its partials, from the pairs that shared the row's items, joined by their maxima and sums.
+__global__ void __launch_bounds__(128) k_prefix_combine(const PaArgs a, uint16_t* __restrict__ out,
+                                                        float* __restrict__ lse) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t r = blockIdx.x;
+  const int b = static_cast<int>(r / a.H), t = static_cast<int>(r / PA_ROWS), tr = static_cast<int>(r % PA_ROWS);
+  const int ob = Cursor::blocks_of(a, b);
+  int id[2], n[2];  // the row's items: its first slot, number of slots
+  int2 sg = make_int2(0, -1);
+  if (!a.multi) {
+    if (a.nP + ob > 0) sg = a.seg[t];
+    id[0] = t + sg.x;
+    n[0] = sg.y - sg.x + 1;
+    id[1] = n[1] = 0;
+  } else {
+    const int qlo = static_cast<int>(static_cast<int64_t>(t) * PA_ROWS / a.H);
+    if (a.nP > 0) sg = a.seg[qlo + 2 * t];
+    id[0] = qlo + 2 * t + sg.x;
+    n[0] = sg.y - sg.x + 1;
+    sg = make_int2(0, -1);
+    if (ob > 0) sg = a.seg[b + 2 * t + 1];
+    id[1] = b + 2 * t + 1 + sg.x;
+    n[1] = sg.y - sg.x + 1;
+  }
+  const int parts = n[0] + n[1];
+  auto slot_row = [&](int i) { return static_cast<int64_t>(i < n[0] ? id[0] + i : id[1] + i - n[0]) * PA_ROWS + tr; };
+  float m = -INFINITY;
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = a.ws_ml[slot_row(i)];
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const int64_t s = slot_row(i);
+    const float2 ml = a.ws_ml[s];
+    if (ml.y == 0.f) continue;
+    const float w = exp2f(ml.x - m);
+    const float4 v = reinterpret_cast<const float4*>(a.ws_o + s * 512)[threadIdx.x];
+    l += w * ml.y;
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
+  }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
-    *reinterpret_cast<uint32_t*>(out + (b * a.H + h) * 512 + 64 * i + 2 * lane) = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  if (lse && lane == 0) lse[b * a.H + h] = l != 0.f ? m + logf(l) : -INFINITY;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 pk;
+  pk.x = *reinterpret_cast<const uint32_t*>(&lo);
+  pk.y = *reinterpret_cast<const uint32_t*>(&hi);
+  reinterpret_cast<uint2*>(out + r * 512)[threadIdx.x] = pk;
+  if (lse && threadIdx.x == 0) lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace
 
-size_t prefix_attn_ws_bytes(int64_t B, int H) { return B > 0 && H > 0 ? 256 : 0; }
+int make_map(CUtensorMap* m, const void* ptr, bool fp8, int64_t rows, int64_t cols, int box_cols, int box_rows);
+
+// Scratch: seg int2 [items] | (max, sum) [slots][128] | O [slots][128][512] fp32, slots = items + 74.
+struct PrefixLayout {
+  int64_t nT, items, slots;
+  bool multi;
+  size_t o_ml, o_o, total;
+};
+static PrefixLayout prefix_ws_layout(int64_t B, int H) {
+  PrefixLayout p;
+  p.nT = cdiv(B * H, PA_ROWS);
+  p.multi = H % PA_ROWS != 0 && B > 1;
+  p.items = p.multi ? B + 2 * p.nT : p.nT;
+  p.slots = p.items + PA_PAIRS;
+  p.o_ml = align_up(static_cast<size_t>(p.items) * 8, 256);
+  p.o_o = p.o_ml + static_cast<size_t>(p.slots) * PA_ROWS * 8;
+  p.total = p.o_o + static_cast<size_t>(p.slots) * PA_ROWS * 512 * 4;
+  return p;
+}
+
+size_t prefix_attn_ws_bytes(int64_t B, int H) { return B > 0 ? prefix_ws_layout(B, H).total : 0; }
 
 int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int64_t Lp, const void* pages,
                        int64_t n_pages, int page, const int32_t* table, int64_t table_ld, const int32_t* own_len,
                        float scale, void* out, float* lse, void* ws, cudaStream_t s) {
-  (void)ws;
+  const PrefixLayout p = prefix_ws_layout(B, H);
+  unsigned char* base = static_cast<unsigned char*>(ws);
   PaArgs a;
-  a.q = static_cast<const uint16_t*>(q);
-  a.prefix = static_cast<const uint16_t*>(prefix);
-  a.pages = static_cast<const uint16_t*>(pages);
   a.own_len = own_len;
   a.table = table;
   a.table_ld = table_ld;
   a.page_shift = 0;
   while ((1 << a.page_shift) < page) ++a.page_shift;
-  a.n_pages = n_pages;
-  a.cap = table_ld * page;
-  a.Lp = Lp;
+  a.box = page < 32 ? page : 32;
+  a.n_pages = static_cast<int>(n_pages);
+  a.cap = static_cast<int>(table_ld * page < 0x7FFFFF00 ? table_ld * page : 0x7FFFFF00);
+  a.B = static_cast<int>(B);
   a.H = H;
-  a.scale = scale;
+  a.BH = B * H;
+  a.nT = static_cast<int>(p.nT);
+  a.multi = p.multi;
+  a.Lp = Lp;
+  a.nP = static_cast<int>(cdiv(Lp, PA_T));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.seg = reinterpret_cast<int2*>(base);
+  a.ws_ml = reinterpret_cast<float2*>(base + p.o_ml);
+  a.ws_o = reinterpret_cast<float*>(base + p.o_o);
+  // an absent part's maps cover the queries: nothing is loaded through them
+  CUtensorMap tq, tk, tv, tp;
+  int st = make_map(&tq, q, false, a.BH, 576, 64, 64);
+  if (st == LSA_OK) st = Lp > 0 ? make_map(&tk, prefix, false, Lp, 576, 64, PA_T / 2) : make_map(&tk, q, false, a.BH, 576, 64, 32);
+  if (st == LSA_OK) st = Lp > 0 ? make_map(&tv, prefix, false, Lp, 576, 64, PA_T) : make_map(&tv, q, false, a.BH, 576, 64, 32);
+  if (st == LSA_OK)
+    st = n_pages > 0 ? make_map(&tp, pages, false, n_pages * page, 576, 64, a.box) : make_map(&tp, q, false, a.BH, 576, 64, 32);
+  if (st != LSA_OK) return st;
   LSA_CUDA_TRY(func_smem_once(reinterpret_cast<const void*>(k_prefix_attn), PA_SMEM));
-  return cuda_status(launch_pdl(k_prefix_attn, dim3(static_cast<unsigned>(B * ((H + 7) / 8))), dim3(PA_THREADS), PA_SMEM,
-                                s, 0u, a, static_cast<uint16_t*>(out), lse));
+  LSA_CUDA_TRY(launch_pdl(k_prefix_attn, dim3(2 * PA_PAIRS), dim3(PA_THREADS), PA_SMEM, s, 0u, tq, tk, tv, tp, a));
+  LSA_CUDA_TRY(launch_pdl(k_prefix_combine, dim3(static_cast<unsigned>(a.BH)), dim3(128), 0, s, 0u, a,
+                          static_cast<uint16_t*>(out), lse));
+  return LSA_OK;
 }
 
-// The kernel's flags, read and cleared: give-up (it has no waits) and device check; -1: CUDA error.
+// The kernel's flags, read and cleared: give-up and device check; -1: CUDA error.
 int take_prefix_flags(int* check) {
-  int c = 0;
+  int v = 0, c = 0;
+  if (cudaMemcpyFromSymbol(&v, g_prefix_timeout, sizeof(int)) != cudaSuccess) return -1;
   if (cudaMemcpyFromSymbol(&c, g_prefix_check, sizeof(int)) != cudaSuccess) return -1;
   const int zero = 0;
+  if (v != 0 && cudaMemcpyToSymbol(g_prefix_timeout, &zero, sizeof(int)) != cudaSuccess) return -1;
   if (c != 0 && cudaMemcpyToSymbol(g_prefix_check, &zero, sizeof(int)) != cudaSuccess) return -1;
   *check = c;
-  return 0;
+  return v;
 }
 
 }  // namespace lsa
