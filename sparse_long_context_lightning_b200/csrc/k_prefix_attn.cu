@@ -318,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       if (c.b < 0) {
         if (one) {
           if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
-          else mbar_arrive_cluster(mapa(smem_u32(&v_full[s]), 0));
+          else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
           const uint32_t bar = mapa(smem_u32(&v_full[s]), 0);
           for (int j = 0; j < 4; ++j)
             tma_load_2d_pair(dst + j * PA_V_KB, &tm_v, bar, 256 * static_cast<int>(rank) + 64 * j, PA_T * c.pos);
@@ -331,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         if (one) {
           if (tail) mbar_expect_tx(vt_full, PA_V_BYTES);
           else if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
-          else mbar_arrive_cluster(mapa(smem_u32(&v_full[s]), 0));
+          else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
         }
         __syncwarp();
         for (int r = 0; r * a.box < PA_T; ++r) {
@@ -354,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (one) mbar_arrive_cluster(mapa(smem_u32(&v_full[s]), 0));
+          if (one) mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
         }
       }
       __syncwarp();
@@ -449,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(c_s_empty + 8 * sb);
+      if (lane == 0) mbar_arrive_pair(c_s_empty + 8 * sb);
       float z[32];
       #pragma unroll
       for (int k = 0; k < 32; ++k) z[k] = k < nvalid ? __uint_as_float(sr[k]) * a.scale_log2 : -INFINITY;
@@ -502,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(c_p_full + 8 * pb);
+      if (lane == 0) mbar_arrive_pair(c_p_full + 8 * pb);
       first = false;
 
       const int id = c.id(a), tile = c.t, own = c.b, ipos = c.item_pos(a), icnt = c.item_cnt(a);

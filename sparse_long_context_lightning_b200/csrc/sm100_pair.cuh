@@ -57,5 +57,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Arrive on a barrier of either CTA of the pair (shared::cluster address).  The release is at CTA scope: what it publishes
+// is this CTA's own tensor memory (loaded to registers before) and its own shared memory (written, then fenced for the
+// async proxy), and the matrix instructions that follow read them where they lie.  A release at cluster scope also
+// waits for the thread's accesses at the L2's distance: about 1000 clocks an arrival, two in every block.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
 }  // namespace sm100
 }  // namespace lsa
