@@ -73,11 +73,14 @@ struct PaArgs {
   float* ws_o;    // [slots][128][512]
 };
 
+// A span: the blocks that one pair walks of a tile's prefix or of one query's pages.  What depends on own_len is read
+// once a span (a load a block cost the softmax 780 clocks of 2100).
 // Items: a tile where all rows belong to one query; else a tile's prefix part, and each of its queries' own part.
 // Their numbers rise along the line of blocks, and so does number + pair: the slot of a (item, pair) partial.
 struct Cursor {
   int t, b;  // tile; query whose own blocks are walked, or -1: the prefix
   int pos, cnt;
+  int len;  // keys of the prefix or of the query's pages
   int qlo, qhi;
 
   static __device__ __forceinline__ int len_of(const PaArgs& a, int b) {
@@ -89,6 +92,7 @@ struct Cursor {
     t = tt;
     b = -1;
     cnt = a.nP;
+    len = static_cast<int>(a.Lp);
     const int64_t r0 = static_cast<int64_t>(tt) * PA_ROWS;
     qlo = static_cast<int>(r0 / a.H);
     qhi = static_cast<int>(min(r0 + PA_ROWS, a.BH) - 1) / a.H;
@@ -98,7 +102,8 @@ struct Cursor {
       pos -= cnt;
       b = b < 0 ? qlo : b + 1;
       if (b <= qhi) {
-        cnt = blocks_of(a, b);
+        len = len_of(a, b);
+        cnt = (len + PA_T - 1) / PA_T;
       } else if (t + 1 < a.nT) {
         tile(a, t + 1);
       } else {  // not reached unless own_len changed since the blocks were counted: rows outside the maps, zeros
@@ -112,6 +117,8 @@ struct Cursor {
     pos = off;
     settle(a);
   }
+  // the span's end among the pair's n blocks, of which i are done
+  __device__ __forceinline__ int span(int i, int n) const { return min(n, cnt - pos > n - i ? n : i + cnt - pos); }
   __device__ __forceinline__ int id(const PaArgs& a) const {
     return !a.multi ? t : (b < 0 ? qlo + 2 * t : b + 2 * t + 1);
   }
@@ -243,13 +250,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   if (warp == PA_KQ_WARP) {
     // ------------------------------------------------------------------ Q and keys
     int loaded = -1, nq = 0;
-    for (int i = 0; i < n && ok; ++i) {
+    for (int i = 0, end; i < n && ok;) {
+     for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
       // page rows of this CTA's 32 keys (lane = box); a box past the end reads as zeros: a row outside the map
       int y = 0;
       if (c.b >= 0) {
         const int key = PA_T * c.pos + 32 * static_cast<int>(rank) + lane * a.box;
         y = PA_NO_ROW;
-        if (lane * a.box < 32 && key < Cursor::len_of(a, c.b)) {
+        if (lane * a.box < 32 && key < c.len) {
           const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
           if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
         }
@@ -289,19 +297,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         }
       }
       __syncwarp();
-      ++c.pos;
-      if (i + 1 < n) c.settle(a);
+     }
+     if (i < n) c.settle(a);
     }
   } else if (warp == PA_V_WARP) {
     // ------------------------------------------------------------------ values: this CTA's 256 dims of all 64 keys
     int ntail = 0;
-    for (int i = 0; i < n && ok; ++i) {
+    for (int i = 0, end; i < n && ok;) {
+     for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
       int y = 0, valid = PA_T;
       if (c.b >= 0) {
-        const int len = Cursor::len_of(a, c.b), key = PA_T * c.pos + lane * a.box;
-        valid = min(PA_T, len - PA_T * c.pos);
+        const int key = PA_T * c.pos + lane * a.box;
+        valid = min(PA_T, c.len - PA_T * c.pos);
         y = PA_NO_ROW;
-        if (lane * a.box < PA_T && key < len) {
+        if (lane * a.box < PA_T && key < c.len) {
           const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
           if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
           else atomicExch(&g_prefix_check, 1);
@@ -358,8 +367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         }
       }
       __syncwarp();
-      ++c.pos;
-      if (i + 1 < n) c.settle(a);
+     }
+     if (i < n) c.settle(a);
     }
   } else if (warp == PA_QK_WARP) {
     // ------------------------------------------------------------------ S = Q K^T (issued by the even CTA)
@@ -367,9 +376,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       const uint64_t qdesc = desc_sw128(smem_u32(q_s));
       int nq = 0;
       bool fresh = true;
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0, end; i < n && ok;) {
+       for (end = c.span(i, n); i < end; ++i, ++c.pos) {
         const int s = i % PA_NK, sb = i % PA_NS;
         if (fresh) ok = mbar_wait_cluster(q_full, nq++ & 1);
+        fresh = false;
         ok = ok && mbar_wait_cluster(&s_empty[sb], ((i / PA_NS) & 1) ^ 1) && mbar_wait_cluster(&k_full[s], (i / PA_NK) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -383,24 +394,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         }
         mma_commit_pair(&k_empty[s]);
         mma_commit_pair(&s_full[sb]);
-        const int t = c.t;
-        ++c.pos;
-        if (i + 1 < n) c.settle(a);
-        fresh = c.t != t;
-        if (fresh) mma_commit_pair(q_empty);
+       }
+       if (i >= n || !ok) break;
+       const int t = c.t;
+       c.settle(a);
+       fresh = c.t != t;
+       if (fresh) mma_commit_pair(q_empty);
       }
     }
   } else if (warp == PA_PV_WARP) {
     // ------------------------------------------------------------------ O += P V (issued by the even CTA)
     if (rank == 0 && n > 0 && elect_one()) {
       int item = -1;
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0, end; i < n && ok;) {
+       uint32_t first = c.id(a) != item;
+       item = c.id(a);
+       for (end = c.span(i, n); i < end; ++i, ++c.pos) {
         const int s = i % PA_NV, pb = i % PA_NP;
         ok = mbar_wait_cluster(&v_full[s], (i / PA_NV) & 1) && mbar_wait_cluster(&p_full[pb], (i / PA_NP) & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t first = c.id(a) != item;
-        item = c.id(a);
         const uint64_t pdesc = desc_sw128(smem_u32(p_s + pb * PA_P_BYTES));
         const uint32_t v_addr = smem_u32(v_s + s * PA_V_BYTES);
         #pragma unroll
@@ -411,10 +424,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
                          desc_sw128_mn(v_addr + 2 * h * PA_V_KB + kk * 16 * 128, PA_V_KB, 1024), IDESC_PV2,
                          kk > 0 || !first);
         }
+        first = 0;
         mma_commit_pair(&v_empty[s]);
         mma_commit_pair(&pv_done[pb]);
-        ++c.pos;
-        if (i + 1 < n) c.settle(a);
+       }
+       if (i < n && ok) c.settle(a);
       }
     }
   } else if (n > 0) {
@@ -430,18 +444,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     float m_used = -INFINITY, l = 0.f;
     bool first = true;
     int seg_pos = c.item_pos(a);
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0, end; i < n;) {
+     // whether this thread's row is one of the span's, and the keys of the span's first block that are this thread's
+     const int64_t gr = static_cast<int64_t>(c.t) * PA_ROWS + trow;
+     const bool live = gr < a.BH && (!a.multi || c.b < 0 || (gr >= static_cast<int64_t>(c.b) * a.H &&
+                                                             gr < static_cast<int64_t>(c.b + 1) * a.H));
+     const int len = live ? c.len : 0;
+     for (end = c.span(i, n); i < end; ++i, ++c.pos) {
       const int sb = i % PA_NS, pb = i % PA_NP;
-      // keys of this thread that exist, and whether its row may see them
-      int nvalid;
-      if (c.b < 0) {
-        nvalid = static_cast<int>(min(static_cast<int64_t>(PA_T), a.Lp - static_cast<int64_t>(PA_T) * c.pos));
-      } else {
-        nvalid = min(PA_T, Cursor::len_of(a, c.b) - PA_T * c.pos);
-        const int64_t gr = static_cast<int64_t>(c.t) * PA_ROWS + trow;
-        if (a.multi && (gr < static_cast<int64_t>(c.b) * a.H || gr >= static_cast<int64_t>(c.b + 1) * a.H)) nvalid = 0;
-      }
-      nvalid -= 32 * kh;
+      const int nvalid = len - PA_T * c.pos - 32 * kh;
       if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&s_full[sb], (i / PA_NS) & 1));
       tc_fence_after();
       uint32_t sr[32];
@@ -504,20 +515,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_pair(c_p_full + 8 * pb);
       first = false;
-
-      const int id = c.id(a), tile = c.t, own = c.b, ipos = c.item_pos(a), icnt = c.item_cnt(a);
-      ++c.pos;
-      if (i + 1 < n) c.settle(a);
-      if (i + 1 < n && c.id(a) == id) continue;
+     }
+      const int id = c.id(a), left = c.item_cnt(a) - c.item_pos(a);
+      if (i < n) {
+        c.settle(a);
+        if (c.id(a) == id) continue;
+      }
       // ---- the item's (or this pair's) last block: the partial sums of its rows
+      const int pb = (i - 1) % PA_NP;
       mx[256 + L] = l;
       named_bar_sync(1, 128);
       const float lt = l + mx[256 + (L ^ 64)];
-      if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], (i / PA_NP) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i - 1) / PA_NP) & 1));
       tc_fence_after();
-      const int64_t gr = static_cast<int64_t>(tile) * PA_ROWS + trow;
-      const bool live = gr < a.BH && (!a.multi || own < 0 || (gr >= static_cast<int64_t>(own) * a.H &&
-                                                               gr < static_cast<int64_t>(own + 1) * a.H));
       const int64_t prow_i = static_cast<int64_t>(id + pair) * PA_ROWS + trow;
       #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
@@ -534,12 +544,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       if (live && kh == 0) a.ws_ml[prow_i] = make_float2(m_used, lt);
       if (rank == 0 && L == 0) {
         if (seg_pos == 0) a.seg[id].x = pair;
-        if (ipos == icnt - 1) a.seg[id].y = pair;
+        if (left == 0) a.seg[id].y = pair;
       }
       m_used = -INFINITY;
       l = 0.f;
       first = true;
-      if (i + 1 < n) seg_pos = c.item_pos(a);
+      if (i < n) seg_pos = c.item_pos(a);
     }
   }
   if (!ok) {
