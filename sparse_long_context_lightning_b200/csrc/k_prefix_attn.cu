@@ -529,18 +529,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i - 1) / PA_NP) & 1));
       tc_fence_after();
       const int64_t prow_i = static_cast<int64_t>(id + pair) * PA_ROWS + trow;
+      // through the warp's quarter of the P buffers (every product is done), 32 rows x 32 columns at a time: a store
+      // instruction writes four whole 128-byte lines in place of 32 rows' 16 bytes (10.7k -> 6.2k clocks a tile)
+      unsigned char* stage = p_s + (warp - PA_SM_WARP) * 4096;
+      const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
+      const int64_t wrow = prow_i - lane;  // the warp's first row
       #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
         uint32_t o[32];
         tmem_ld32(tlane + PT_O + 32 * k, o);
         tmem_ld_wait();
-        if (live) {
-          uint4* d = reinterpret_cast<uint4*>(a.ws_o + prow_i * 512 + 256 * kh + 32 * k);
-          #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        #pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        __syncwarp();
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = 4 * e + (lane >> 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if ((live_rows >> r) & 1)
+            *reinterpret_cast<uint4*>(a.ws_o + (wrow + r) * 512 + 256 * kh + 32 * k + 4 * (lane & 7)) = v;
         }
+        __syncwarp();
       }
       tc_fence_before();
+      named_bar_sync(1, 128);  // the next block's probabilities go to the same buffers
       if (live && kh == 0) a.ws_ml[prow_i] = make_float2(m_used, lt);
       if (rank == 0 && L == 0) {
         if (seg_pos == 0) a.seg[id].x = pair;
@@ -571,8 +585,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
 }
 
 // One block a row (b, h): its partials, from the pairs that shared the row's items, joined by their maxima and sums.
-__global__ void __launch_bounds__(128) k_prefix_combine(const PaArgs a, uint16_t* __restrict__ out,
-                                                        float* __restrict__ lse) {
+// G groups of 128 threads take the partials in turn (four columns a thread), the weights are formed once a block: a row
+// behind a long prefix has up to 74 partials and few other rows to hide its loads behind.
+template <int G>
+__global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint16_t* __restrict__ out,
+                                                            float* __restrict__ lse) {
+  constexpr int MAXP = 2 * PA_PAIRS;
+  __shared__ float wt[MAXP];
+  __shared__ float4 acc_s[G > 1 ? (G - 1) * 128 : 1];
+  __shared__ float red[2 * 4 * G];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t r = blockIdx.x;
@@ -587,34 +608,66 @@ __global__ void __launch_bounds__(128) k_prefix_combine(const PaArgs a, uint16_t
     id[1] = n[1] = 0;
   } else {
     const int qlo = static_cast<int>(static_cast<int64_t>(t) * PA_ROWS / a.H);
+    int2 sh = make_int2(0, -1);
     if (a.nP > 0) sg = a.seg[qlo + 2 * t];
+    if (ob > 0) sh = a.seg[b + 2 * t + 1];
     id[0] = qlo + 2 * t + sg.x;
     n[0] = sg.y - sg.x + 1;
-    sg = make_int2(0, -1);
-    if (ob > 0) sg = a.seg[b + 2 * t + 1];
-    id[1] = b + 2 * t + 1 + sg.x;
-    n[1] = sg.y - sg.x + 1;
+    id[1] = b + 2 * t + 1 + sh.x;
+    n[1] = sh.y - sh.x + 1;
   }
-  const int parts = n[0] + n[1];
+  const int parts = min(n[0] + n[1], MAXP);
   auto slot_row = [&](int i) { return static_cast<int64_t>(i < n[0] ? id[0] + i : id[1] + i - n[0]) * PA_ROWS + tr; };
+  // the parts' maxima and sums: part tid (and tid + 128 G where there are that many)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float m = -INFINITY;
-  for (int i = 0; i < parts; ++i) {
+  for (int i = tid; i < parts; i += 128 * G) {
     const float2 ml = a.ws_ml[slot_row(i)];
     if (ml.y != 0.f) m = fmaxf(m, ml.x);
   }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = warp_max(m);
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  #pragma unroll
+  for (int w = 0; w < 4 * G; ++w) m = fmaxf(m, red[w]);
   float l = 0.f;
-  for (int i = 0; i < parts; ++i) {
-    const int64_t s = slot_row(i);
-    const float2 ml = a.ws_ml[s];
-    if (ml.y == 0.f) continue;
-    const float w = exp2f(ml.x - m);
-    const float4 v = reinterpret_cast<const float4*>(a.ws_o + s * 512)[threadIdx.x];
+  for (int i = tid; i < parts; i += 128 * G) {
+    const float2 ml = a.ws_ml[slot_row(i)];
+    const float w = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
+    wt[i] = w;
     l += w * ml.y;
-    acc.x += w * v.x;
-    acc.y += w * v.y;
-    acc.z += w * v.z;
-    acc.w += w * v.w;
+  }
+  l = warp_sum(l);
+  if (lane == 0) red[4 * G + warp] = l;
+  __syncthreads();
+  l = 0.f;
+  #pragma unroll
+  for (int w = 0; w < 4 * G; ++w) l += red[4 * G + w];
+  const int col = tid & 127;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll 4
+  for (int i = tid >> 7; i < parts; i += G) {
+    const float w = wt[i];
+    const float4 v = reinterpret_cast<const float4*>(a.ws_o + slot_row(i) * 512)[col];
+    if (w != 0.f) {  // a partial without keys holds nothing
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+  }
+  if (G > 1) {
+    if (tid >= 128) acc_s[tid - 128] = acc;
+    __syncthreads();
+    if (tid >= 128) return;
+    #pragma unroll
+    for (int g = 0; g < G - 1; ++g) {
+      const float4 v = acc_s[g * 128 + tid];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
@@ -622,8 +675,8 @@ __global__ void __launch_bounds__(128) k_prefix_combine(const PaArgs a, uint16_t
   uint2 pk;
   pk.x = *reinterpret_cast<const uint32_t*>(&lo);
   pk.y = *reinterpret_cast<const uint32_t*>(&hi);
-  reinterpret_cast<uint2*>(out + r * 512)[threadIdx.x] = pk;
-  if (lse && threadIdx.x == 0) lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  reinterpret_cast<uint2*>(out + r * 512)[tid] = pk;
+  if (lse && tid == 0) lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace
@@ -685,9 +738,10 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   if (st != LSA_OK) return st;
   LSA_CUDA_TRY(func_smem_once(reinterpret_cast<const void*>(k_prefix_attn), PA_SMEM));
   LSA_CUDA_TRY(launch_pdl(k_prefix_attn, dim3(2 * PA_PAIRS), dim3(PA_THREADS), PA_SMEM, s, 0u, tq, tk, tv, tp, a));
-  LSA_CUDA_TRY(launch_pdl(k_prefix_combine, dim3(static_cast<unsigned>(a.BH)), dim3(128), 0, s, 0u, a,
-                          static_cast<uint16_t*>(out), lse));
-  return LSA_OK;
+  // a row has about 74 / tiles partials
+  const dim3 rows(static_cast<unsigned>(a.BH));
+  return cuda_status(a.nT <= 8 ? launch_pdl(k_prefix_combine<4>, rows, dim3(512), 0, s, 0u, a, static_cast<uint16_t*>(out), lse)
+                               : launch_pdl(k_prefix_combine<1>, rows, dim3(128), 0, s, 0u, a, static_cast<uint16_t*>(out), lse));
 }
 
 // The kernel's flags, read and cleared: give-up and device check; -1: CUDA error.
