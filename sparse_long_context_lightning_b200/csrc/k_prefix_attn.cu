@@ -4,19 +4,21 @@
 // over the Lp rows of the prefix (the same for every query) and own_len[b] rows behind them (block table).
 //
 // The batch's B * H query rows are cut into tiles of 128, whatever H is, and every tile walks the prefix in blocks of
-// 64 keys, then the blocks of its own queries' pages, with one running maximum and sum per row.  2 (576 + 512) flops a
+// 128 keys, then the blocks of its own queries' pages, with one running maximum and sum per row.  2 (576 + 512) flops a
 // (row, key) against 1152 bytes a key: from about 190 rows on the matrix units bound it, below that the prefix's bytes.
 //
 // A CTA pair (cluster of two, tcgen05 cta_group::2, M = 128) takes a tile: each CTA has 64 rows of Q, their logits,
-// probabilities and output, so the softmax never leaves the CTA, and feeds half of every B operand: 32 of a block's 64
-// keys for S = Q K^T (N = 64) and 256 of the 512 value dims for O += P V (two N = 256 instructions a 16 keys).  A
+// probabilities and output, so the softmax never leaves the CTA, and feeds half of every B operand: 64 of a block's 128
+// keys for S = Q K^T (N = 128) and 256 of the 512 value dims for O += P V (two N = 256 instructions a 16 keys).  A
 // 128 x 512 fp32 output would fill a CTA's tensor memory; the pair's 64 rows a CTA take half of it and leave room for
 // four buffers of S, so the logits run ahead of the softmax.  The same bytes cannot serve as keys and as values here
 // (one descriptor gives both CTAs' halves of B, and the halves are cut along different axes), so a block is loaded
-// twice, 1088 bytes a key and CTA, the second time from L2: this loop without its softmax, fed from L2, ran at 1440 to
-// 1545 TFLOP/s, the same matrix instructions without loads at 1531, the loads alone at 20 TB/s.
-// N = 64 costs 22.6 clocks a key and SM against 17.0 at N = 128 (A is read again for every block), but two stages of
-// 128 keys do not fit beside Q; 96 keys in one stage each ran at 1080 to 1150.
+// twice, 1088 bytes a key and CTA, the second time from L2.  Keys arrive in stages of 64 keys x 192 dims (three a
+// block) and values in stages of 32 keys, each by one instruction of a three-dimensional map: a warp that issues a load
+// waits about 200 clocks before its next, so nine small loads a block held the block at 3750 clocks.  With 64-key
+// blocks (N = 64, A read again for each, 22.6 clocks a key and SM against 17.0) the same batch took 529 us against 470.
+// 16 queries of 128 heads behind 131072 rows: 470 us, 1240 TFLOP/s; 64 queries behind 32749: 414 us, 1430 TFLOP/s,
+// where the GPU's power limit holds the clock near 1.4 GHz (cuBLAS sustains 1385 there).
 //
 // Work is cut evenly: the blocks of all tiles, in order, are one line that 74 pairs divide; a tile that spans pairs
 // leaves partial sums (fp32) that k_prefix_combine joins.  Where a tile holds several queries (H not a multiple of 128),
@@ -32,22 +34,30 @@ using namespace sm100;
 __device__ int g_prefix_timeout;  // set when a bounded wait gave up
 __device__ int g_prefix_check;    // set when own_len was outside [0, the table's columns * page] or a page id was bad
 
-constexpr int PA_THREADS = 256;
-constexpr int PA_KQ_WARP = 0, PA_QK_WARP = 1, PA_PV_WARP = 2, PA_V_WARP = 3, PA_SM_WARP = 4;
+constexpr int PA_THREADS = 384;
+constexpr int PA_KQ_WARP = 0, PA_QK_WARP = 1, PA_PV_WARP = 2, PA_V_WARP = 3, PA_SM_WARP = 4, PA_SM_WARPS = 8;
 constexpr int PA_PAIRS = 74;  // one pair on every two of the 148 SMs
-constexpr int PA_T = 64;      // keys of a block
+constexpr int PA_T = 128;     // keys of a block
 constexpr int PA_ROWS = 128;  // query rows of a tile
-constexpr int PA_NK = 2, PA_NV = 2, PA_NS = 4, PA_NP = 2;
-constexpr int PA_Q_KB = 64 * 128;         // 64 rows x 64 dims
-constexpr int PA_Q_BYTES = 9 * PA_Q_KB;   // 72 KB
-constexpr int PA_P_BYTES = 64 * 128;      // 64 rows x 64 keys
-constexpr int PA_K_KB = PA_T / 2 * 128;   // 32 keys x 64 dims
-constexpr int PA_K_BYTES = 9 * PA_K_KB;   // 36 KB
-constexpr int PA_V_KB = PA_T * 128;       // 64 keys x 64 dims
-constexpr int PA_V_BYTES = 4 * PA_V_KB;   // 32 KB
-constexpr int PA_SMEM = 1024 + PA_Q_BYTES + PA_NP * PA_P_BYTES + PA_NK * PA_K_BYTES + PA_NV * PA_V_BYTES + 3 * 512 + 512;
+#ifndef PA_NK_
+#define PA_NK_ 3
+#define PA_NV_ 4
+#endif
+constexpr int PA_NK = PA_NK_, PA_NV = PA_NV_, PA_NS = 4, PA_NP = 1;
+constexpr int PA_Q_KB = 64 * 128;        // 64 rows x 64 dims
+constexpr int PA_Q_BYTES = 9 * PA_Q_KB;  // 72 KB
+constexpr int PA_P_KB = 64 * 128;        // 64 rows x 64 keys
+constexpr int PA_P_BYTES = 2 * PA_P_KB;
+constexpr int PA_KT = PA_T / 2;          // keys of a block that this CTA feeds to S
+constexpr int PA_KS = 3;                 // 64-dim parts of a stage of keys
+constexpr int PA_K_KB = PA_KT * 128;     // 64 keys x 64 dims
+constexpr int PA_K_BYTES = PA_KS * PA_K_KB;
+constexpr int PA_VT = 32;                // keys of a stage of values
+constexpr int PA_V_KB = PA_VT * 128;     // 32 keys x 64 dims
+constexpr int PA_V_BYTES = 4 * PA_V_KB;
+constexpr int PA_SMEM = PA_Q_BYTES + PA_NP * PA_P_BYTES + PA_NK * PA_K_BYTES + PA_NV * PA_V_BYTES + 2 * 1024 + 512;
 static_assert(PA_SMEM <= 232448, "shared memory");
-constexpr uint32_t PT_O = 0, PT_S = 256;  // TMEM columns: O [0, 256), S buffers of 32 from 256
+constexpr uint32_t PT_O = 0, PT_S = 256;  // TMEM columns: O [0, 256), S buffers of 64 from 256
 constexpr uint32_t IDESC_QK = idesc_mma(128, PA_T, 1u, 0u);
 constexpr uint32_t IDESC_PV2 = idesc_mma(128, 256, 1u, 1u);
 constexpr float PA_RESCALE = 8.f;
@@ -58,7 +68,7 @@ struct PaArgs {
   const int32_t* table;    // [B, table_ld] page ids
   int64_t table_ld;
   int page_shift;  // log2 of the page size
-  int box;         // rows of a page box: min(page, 32)
+  int kbox, vbox;  // rows of a page box: min(page, 64 or 32) of keys, min(page, 32) of values
   int n_pages;
   int cap;  // most own tokens: the table's columns * page (clamped to int)
   int B, H;
@@ -137,15 +147,15 @@ __device__ __forceinline__ int tile_blocks(const PaArgs& a, int t) {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     k_prefix_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_p, const PaArgs a) {
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pk,
+                  const __grid_constant__ CUtensorMap tm_pv, const PaArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* q_s = base;
+  unsigned char* q_s = smem_raw;
   unsigned char* p_s = q_s + PA_Q_BYTES;
   unsigned char* k_s = p_s + PA_NP * PA_P_BYTES;
   unsigned char* v_s = k_s + PA_NK * PA_K_BYTES;
-  float* mx = reinterpret_cast<float*>(v_s + PA_NV * PA_V_BYTES);  // [3][128]: row maxima of two blocks, row sums
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(mx + 3 * 128);
+  float* mx = reinterpret_cast<float*>(v_s + PA_NV * PA_V_BYTES);  // [2][256]: row maxima of a block, row sums
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(mx + 2 * 256);
   uint64_t* q_empty = q_full + 1;
   uint64_t* k_full = q_empty + 1;
   uint64_t* k_empty = k_full + PA_NK;
@@ -155,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   uint64_t* s_empty = s_full + PA_NS;
   uint64_t* p_full = s_empty + PA_NS;
   uint64_t* pv_done = p_full + PA_NP;
-  uint64_t* vt_full = pv_done + PA_NP;  // this CTA's values of a block whose last page is partly filled
+  uint64_t* vt_full = pv_done + PA_NP;  // this CTA's values of a stage whose last page is partly filled
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(vt_full + 1);
   int* start_s = reinterpret_cast<int*>(tmem_holder + 1);  // this pair's first tile, block of it, number of blocks
   int* abort_flag = start_s + 3;
@@ -178,10 +188,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     }
     for (int i = 0; i < PA_NS; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 8);  // the softmax warps of both CTAs
+      mbar_init(&s_empty[i], 2 * PA_SM_WARPS);  // the softmax warps of both CTAs
     }
     for (int i = 0; i < PA_NP; ++i) {
-      mbar_init(&p_full[i], 8);
+      mbar_init(&p_full[i], 2 * PA_SM_WARPS);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(vt_full, 1);
@@ -248,274 +258,303 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   bool ok = true;
 
   if (warp == PA_KQ_WARP) {
-    // ------------------------------------------------------------------ Q and keys
+    // ------------------------------------------------------------------ Q and keys: stages of 64 keys x 64 dims
     int loaded = -1, nq = 0;
+    uint32_t s = 0, phase = 1;
     for (int i = 0, end; i < n && ok;) {
-     for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
-      // page rows of this CTA's 32 keys (lane = box); a box past the end reads as zeros: a row outside the map
-      int y = 0;
-      if (c.b >= 0) {
-        const int key = PA_T * c.pos + 32 * static_cast<int>(rank) + lane * a.box;
-        y = PA_NO_ROW;
-        if (lane * a.box < 32 && key < c.len) {
-          const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
-          if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+      for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+        const int key0 = PA_T * c.pos + PA_KT * static_cast<int>(rank);
+        // page rows of this CTA's keys (lane = box); a box past the end reads as zeros: a row outside the map
+        int y = PA_NO_ROW;
+        if (c.b >= 0) {
+          const int key = key0 + lane * a.kbox;
+          if (lane * a.kbox < PA_KT && key < c.len) {
+            const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
+            if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+          }
+        }
+        const bool one = elect_one();
+        if (c.t != loaded) {
+          ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1));
+          if (ok && one) {
+            if (rank == 0) mbar_expect_tx(q_full, 2 * PA_Q_BYTES);
+            const uint32_t bar = mapa(smem_u32(q_full), 0);
+            tma_load_3d_pair(q_s, &tm_q, bar, 0, c.t * PA_ROWS + 64 * static_cast<int>(rank), 0);
+          }
+          __syncwarp();
+          loaded = c.t;
+          ++nq;
+        }
+        for (int j = 0; j < 9; j += PA_KS) {
+          ok = __all_sync(0xffffffffu, mbar_spin(&k_empty[s], phase));
+          if (!ok) break;
+          const uint32_t bar = mapa(smem_u32(&k_full[s]), 0);
+          unsigned char* dst = k_s + s * PA_K_BYTES;
+          if (one && rank == 0) mbar_expect_tx(&k_full[s], 2 * PA_K_BYTES);
+          if (c.b < 0) {
+            if (one) tma_load_3d_pair(dst, &tm_k, bar, 0, key0, j);
+          } else {
+            if (a.kbox == PA_KT) {
+              const int y0 = __shfl_sync(0xffffffffu, y, 0);
+              if (one) tma_load_3d_pair(dst, &tm_pk, bar, 0, y0, j);
+            } else {
+              for (int r = 0; r * a.kbox < PA_KT; ++r) {
+                const int yr = __shfl_sync(0xffffffffu, y, r);
+                if (one)
+                  for (int e = 0; e < PA_KS; ++e)
+                    tma_load_3d_pair(dst + e * PA_K_KB + r * a.kbox * 128, &tm_pk, bar, 0, yr, j + e);
+              }
+            }
+          }
+          __syncwarp();
+          if (++s == PA_NK) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
-      if (c.t != loaded) {
-        ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1));
-        if (ok && elect_one()) {
-          if (rank == 0) mbar_expect_tx(q_full, 2 * PA_Q_BYTES);
-          const uint32_t bar = mapa(smem_u32(q_full), 0);
-          for (int j = 0; j < 9; ++j)
-            tma_load_2d_pair(q_s + j * PA_Q_KB, &tm_q, bar, 64 * j, c.t * PA_ROWS + 64 * static_cast<int>(rank));
-        }
-        __syncwarp();
-        loaded = c.t;
-        ++nq;
-      }
-      const int s = i % PA_NK;
-      ok = ok && mbar_spin(&k_empty[s], ((i / PA_NK) & 1) ^ 1);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      const uint32_t bar = mapa(smem_u32(&k_full[s]), 0);
-      unsigned char* dst = k_s + s * PA_K_BYTES;
-      const bool one = elect_one();
-      if (one && rank == 0) mbar_expect_tx(&k_full[s], 2 * PA_K_BYTES);
-      if (c.b < 0) {
-        if (one)
-          for (int j = 0; j < 9; ++j)
-            tma_load_2d_pair(dst + j * PA_K_KB, &tm_k, bar, 64 * j, PA_T * c.pos + 32 * static_cast<int>(rank));
-      } else {
-        for (int r = 0; r * a.box < 32; ++r) {
-          const int yr = __shfl_sync(0xffffffffu, y, r);
-          if (one)
-            for (int j = 0; j < 9; ++j)
-              tma_load_2d_pair(dst + j * PA_K_KB + r * a.box * 128, &tm_p, bar, 64 * j, yr);
-        }
-      }
-      __syncwarp();
-     }
-     if (i < n) c.settle(a);
+      if (i < n && ok) c.settle(a);
     }
   } else if (warp == PA_V_WARP) {
-    // ------------------------------------------------------------------ values: this CTA's 256 dims of all 64 keys
+    // ------------------------------------------------------------------ values: this CTA's 256 dims, stages of 32 keys
     int ntail = 0;
+    uint32_t s = 0, phase = 1;
     for (int i = 0, end; i < n && ok;) {
-     for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
-      int y = 0, valid = PA_T;
-      if (c.b >= 0) {
-        const int key = PA_T * c.pos + lane * a.box;
-        valid = min(PA_T, c.len - PA_T * c.pos);
-        y = PA_NO_ROW;
-        if (lane * a.box < PA_T && key < c.len) {
-          const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
-          if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-          else atomicExch(&g_prefix_check, 1);
-        }
-      }
-      const int s = i % PA_NV;
-      ok = mbar_spin(&v_empty[s], ((i / PA_NV) & 1) ^ 1);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      unsigned char* dst = v_s + s * PA_V_BYTES;
-      const bool one = elect_one();
-      if (c.b < 0) {
-        if (one) {
-          if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
-          else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
-          const uint32_t bar = mapa(smem_u32(&v_full[s]), 0);
-          for (int j = 0; j < 4; ++j)
-            tma_load_2d_pair(dst + j * PA_V_KB, &tm_v, bar, 256 * static_cast<int>(rank) + 64 * j, PA_T * c.pos);
-        }
-      } else {
-        // rows of a partly filled box behind the sequence's end hold anything (NaN too) and would meet p = 0 in the
-        // product: such a block lands on this CTA's own barrier, has those rows zeroed, and is then handed over
-        const bool tail = (valid & (a.box - 1)) != 0;
-        const uint32_t bar = tail ? mapa(smem_u32(vt_full), rank) : mapa(smem_u32(&v_full[s]), 0);
-        if (one) {
-          if (tail) mbar_expect_tx(vt_full, PA_V_BYTES);
-          else if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
-          else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
-        }
-        __syncwarp();
-        for (int r = 0; r * a.box < PA_T; ++r) {
-          const int yr = __shfl_sync(0xffffffffu, y, r);
-          if (one)
-            for (int j = 0; j < 4; ++j)
-              tma_load_2d_pair(dst + j * PA_V_KB + r * a.box * 128, &tm_p, bar, 256 * static_cast<int>(rank) + 64 * j, yr);
-        }
-        if (tail) {
-          ok = mbar_wait(vt_full, ntail & 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
+      for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+        const int key0 = PA_T * c.pos;
+        int y = PA_NO_ROW;
+        if (c.b >= 0) {
+          const int key = key0 + lane * a.vbox;
+          if (lane * a.vbox < PA_T && key < c.len) {
+            const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
+            if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+            else atomicExch(&g_prefix_check, 1);
           }
-          ++ntail;
-          const int rows = min(PA_T, (valid + a.box - 1) / a.box * a.box) - valid;
-          for (int x = lane; x < 4 * rows * 8; x += 32) {
-            const int j = x / (rows * 8), e = x - j * rows * 8;
-            *reinterpret_cast<uint4*>(dst + j * PA_V_KB + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+        const bool one = elect_one();
+        for (int k = 0; k < PA_T && key0 + k < c.len; k += PA_VT) {
+          ok = __all_sync(0xffffffffu, mbar_spin(&v_empty[s], phase));
+          if (!ok) break;
+          unsigned char* dst = v_s + s * PA_V_BYTES;
+          if (c.b < 0) {
+            if (one) {
+              if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
+              else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
+              const uint32_t bar = mapa(smem_u32(&v_full[s]), 0);
+              tma_load_3d_pair(dst, &tm_v, bar, 0, key0 + k, 4 * static_cast<int>(rank));
+            }
+          } else {
+            // rows of a partly filled box behind the sequence's end hold anything (NaN too) and would meet p = 0 in the
+            // product: such a stage lands on this CTA's own barrier, has those rows zeroed, and is then handed over
+            const int valid = min(PA_VT, c.len - key0 - k);
+            const bool tail = (valid & (a.vbox - 1)) != 0;
+            const uint32_t bar = tail ? mapa(smem_u32(vt_full), rank) : mapa(smem_u32(&v_full[s]), 0);
+            if (one) {
+              if (tail) mbar_expect_tx(vt_full, PA_V_BYTES);
+              else if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
+              else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
+            }
+            __syncwarp();
+            if (a.vbox == PA_VT) {
+              const int y0 = __shfl_sync(0xffffffffu, y, k / PA_VT);
+              if (one) tma_load_3d_pair(dst, &tm_pv, bar, 0, y0, 4 * static_cast<int>(rank));
+            } else {
+              for (int r = 0; r * a.vbox < PA_VT; ++r) {
+                const int yr = __shfl_sync(0xffffffffu, y, k / a.vbox + r);
+                if (one)
+                  for (int j = 0; j < 4; ++j)
+                    tma_load_3d_pair(dst + j * PA_V_KB + r * a.vbox * 128, &tm_pv, bar, 0, yr, 4 * static_cast<int>(rank) + j);
+              }
+            }
+            if (tail) {
+              ok = __all_sync(0xffffffffu, mbar_wait(vt_full, ntail & 1));
+              if (!ok) break;
+              ++ntail;
+              const int rows = (valid + a.vbox - 1) / a.vbox * a.vbox - valid;
+              for (int x = lane; x < 4 * rows * 8; x += 32) {
+                const int j = x / (rows * 8), e = x - j * rows * 8;
+                *reinterpret_cast<uint4*>(dst + j * PA_V_KB + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (one) mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
+            }
           }
-          fence_proxy_async_smem();
           __syncwarp();
-          if (one) mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
+          if (++s == PA_NV) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
-      __syncwarp();
-     }
-     if (i < n) c.settle(a);
+      if (i < n && ok) c.settle(a);
     }
   } else if (warp == PA_QK_WARP) {
     // ------------------------------------------------------------------ S = Q K^T (issued by the even CTA)
     if (rank == 0 && n > 0 && elect_one()) {
-      const uint64_t qdesc = desc_sw128(smem_u32(q_s));
+      const uint64_t qdesc = desc_sw128(smem_u32(q_s)), kdesc = desc_sw128(smem_u32(k_s));
       int nq = 0;
       bool fresh = true;
+      uint32_t s = 0, phase = 0;
       for (int i = 0, end; i < n && ok;) {
-       for (end = c.span(i, n); i < end; ++i, ++c.pos) {
-        const int s = i % PA_NK, sb = i % PA_NS;
-        if (fresh) ok = mbar_wait_cluster(q_full, nq++ & 1);
-        fresh = false;
-        ok = ok && mbar_wait_cluster(&s_empty[sb], ((i / PA_NS) & 1) ^ 1) && mbar_wait_cluster(&k_full[s], (i / PA_NK) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t kdesc = desc_sw128(smem_u32(k_s + s * PA_K_BYTES));
-        #pragma unroll
-        for (int kb = 0; kb < 9; ++kb) {
+        for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+          const int sb = i % PA_NS;
+          if (fresh) ok = mbar_wait_cluster(q_full, nq++ & 1);
+          fresh = false;
+          ok = ok && mbar_wait_cluster(&s_empty[sb], ((i / PA_NS) & 1) ^ 1);
           #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_pair(tmem + PT_S + sb * (PA_T / 2), qdesc + ((kb * PA_Q_KB + kk * 32) >> 4),
-                         kdesc + ((kb * PA_K_KB + kk * 32) >> 4), IDESC_QK, (kb | kk) != 0);
+          for (int kb = 0; kb < 9; kb += PA_KS) {
+            ok = ok && mbar_wait_cluster(&k_full[s], phase);
+            if (!ok) break;
+            tc_fence_after();
+            #pragma unroll
+            for (int kk = 0; kk < 4 * PA_KS; ++kk)
+              mma_f16_pair(tmem + PT_S + sb * PA_KT, qdesc + (((kb + kk / 4) * PA_Q_KB + kk % 4 * 32) >> 4),
+                           kdesc + ((s * PA_K_BYTES + kk / 4 * PA_K_KB + kk % 4 * 32) >> 4), IDESC_QK, (kb | kk) != 0);
+            mma_commit_pair(&k_empty[s]);
+            if (++s == PA_NK) {
+              s = 0;
+              phase ^= 1;
+            }
+          }
+          if (ok) mma_commit_pair(&s_full[sb]);
         }
-        mma_commit_pair(&k_empty[s]);
-        mma_commit_pair(&s_full[sb]);
-       }
-       if (i >= n || !ok) break;
-       const int t = c.t;
-       c.settle(a);
-       fresh = c.t != t;
-       if (fresh) mma_commit_pair(q_empty);
+        if (i >= n || !ok) break;
+        const int t = c.t;
+        c.settle(a);
+        fresh = c.t != t;
+        if (fresh) mma_commit_pair(q_empty);
       }
     }
   } else if (warp == PA_PV_WARP) {
     // ------------------------------------------------------------------ O += P V (issued by the even CTA)
     if (rank == 0 && n > 0 && elect_one()) {
+      const uint64_t pdesc = desc_sw128(smem_u32(p_s)), vdesc = desc_sw128_mn(smem_u32(v_s), PA_V_KB, 1024);
       int item = -1;
+      uint32_t s = 0, phase = 0;
       for (int i = 0, end; i < n && ok;) {
-       uint32_t first = c.id(a) != item;
-       item = c.id(a);
-       for (end = c.span(i, n); i < end; ++i, ++c.pos) {
-        const int s = i % PA_NV, pb = i % PA_NP;
-        ok = mbar_wait_cluster(&v_full[s], (i / PA_NV) & 1) && mbar_wait_cluster(&p_full[pb], (i / PA_NP) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t pdesc = desc_sw128(smem_u32(p_s + pb * PA_P_BYTES));
-        const uint32_t v_addr = smem_u32(v_s + s * PA_V_BYTES);
-        #pragma unroll
-        for (int kk = 0; kk < PA_T / 16; ++kk) {
+        uint32_t acc = c.id(a) == item;
+        item = c.id(a);
+        for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+          const int pb = i % PA_NP;
+          ok = mbar_wait_cluster(&p_full[pb], (i / PA_NP) & 1);
           #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_f16_pair(tmem + PT_O + h * 128, pdesc + ((kk * 32) >> 4),
-                         desc_sw128_mn(v_addr + 2 * h * PA_V_KB + kk * 16 * 128, PA_V_KB, 1024), IDESC_PV2,
-                         kk > 0 || !first);
+          for (int k = 0; k < PA_T / PA_VT; ++k) {
+            if (PA_T * c.pos + PA_VT * k >= c.len) break;
+            ok = ok && mbar_wait_cluster(&v_full[s], phase);
+            if (!ok) break;
+            tc_fence_after();
+            #pragma unroll
+            for (int kk = 0; kk < PA_VT / 16; ++kk) {
+              const uint64_t pd = pdesc + ((pb * PA_P_BYTES + (k >> 1) * PA_P_KB + ((k & 1) * 2 + kk) * 32) >> 4);
+              #pragma unroll
+              for (int h = 0; h < 2; ++h)
+                mma_f16_pair(tmem + PT_O + h * 128, pd, vdesc + ((s * PA_V_BYTES + 2 * h * PA_V_KB + kk * 2048) >> 4),
+                             IDESC_PV2, acc);
+              acc = 1;
+            }
+            mma_commit_pair(&v_empty[s]);
+            if (++s == PA_NV) {
+              s = 0;
+              phase ^= 1;
+            }
+          }
+          if (ok) mma_commit_pair(&pv_done[pb]);
         }
-        first = 0;
-        mma_commit_pair(&v_empty[s]);
-        mma_commit_pair(&pv_done[pb]);
-       }
-       if (i < n && ok) c.settle(a);
+        if (i < n && ok) c.settle(a);
       }
     }
   } else if (n > 0) {
     // ------------------------------------------------------------------ softmax and partial sums
-    // Thread L: row L % 64 of this CTA, keys [32 (L / 64), 32 (L / 64) + 32) of a block, value dims
-    // [256 (L / 64), 256 (L / 64) + 256).  A wait that gave up is not waited for again, but the loop goes on: the
-    // four warps meet at a named barrier in every block.
-    const int L = (warp - PA_SM_WARP) * 32 + lane;
+    // Thread (L, ch): row L % 64 of this CTA, keys [64 kh + 32 ch, + 32) of a block and value dims [256 kh + 128 ch, + 128),
+    // kh = L / 64.  A wait that gave up is not waited for again, but the loop goes on: the eight warps meet at a named
+    // barrier in every block.
+    const int ch = (warp - PA_SM_WARP) >> 2;
+    const int L = ((warp - PA_SM_WARP) & 3) * 32 + lane;
     const int row = L & 63, kh = L >> 6;
     const int trow = 64 * static_cast<int>(rank) + row;  // row of the tile
-    const uint32_t tlane = tmem + (static_cast<uint32_t>((warp - PA_SM_WARP) * 32) << 16);
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(((warp - PA_SM_WARP) & 3) * 32) << 16);
+    const uint32_t t_s = tlane + PT_S + 32 * ch, t_o = tlane + PT_O + 128 * ch;
     const uint32_t c_s_empty = mapa(smem_u32(s_empty), 0), c_p_full = mapa(smem_u32(p_full), 0);
+    // the row's other three quarters
+    auto row_max = [&](const float* m, float v) {
+      return fmaxf(fmaxf(v, m[128 * (ch ^ 1) + L]), fmaxf(m[L ^ 64], m[128 + (L ^ 64)]));
+    };
     float m_used = -INFINITY, l = 0.f;
     bool first = true;
     int seg_pos = c.item_pos(a);
     for (int i = 0, end; i < n;) {
-     // whether this thread's row is one of the span's, and the keys of the span's first block that are this thread's
-     const int64_t gr = static_cast<int64_t>(c.t) * PA_ROWS + trow;
-     const bool live = gr < a.BH && (!a.multi || c.b < 0 || (gr >= static_cast<int64_t>(c.b) * a.H &&
-                                                             gr < static_cast<int64_t>(c.b + 1) * a.H));
-     const int len = live ? c.len : 0;
-     for (end = c.span(i, n); i < end; ++i, ++c.pos) {
-      const int sb = i % PA_NS, pb = i % PA_NP;
-      const int nvalid = len - PA_T * c.pos - 32 * kh;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&s_full[sb], (i / PA_NS) & 1));
-      tc_fence_after();
-      uint32_t sr[32];
-      tmem_ld32(tlane + PT_S + sb * (PA_T / 2), sr);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair(c_s_empty + 8 * sb);
-      float z[32];
-      #pragma unroll
-      for (int k = 0; k < 32; ++k) z[k] = k < nvalid ? __uint_as_float(sr[k]) * a.scale_log2 : -INFINITY;
-      float m4[4] = {z[0], z[1], z[2], z[3]};
-      #pragma unroll
-      for (int k = 4; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], z[k]);
-      float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      // the row's other 32 keys are another warp's
-      mx[128 * (i & 1) + L] = mt;
-      named_bar_sync(1, 128);
-      mt = fmaxf(mt, mx[128 * (i & 1) + (L ^ 64)]);
-      float alpha = 1.f;
-      if (mt > m_used + PA_RESCALE || (first && mt > m_used)) {
-        alpha = ex2_approx(m_used - mt);  // 0 from -inf
-        m_used = mt;
-      }
-      const float m_ref = m_used == -INFINITY ? 0.f : m_used;
-      uint32_t pk[16];
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-      #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        const float p0 = ex2_approx(z[k] - m_ref), p1 = ex2_approx(z[k + 1] - m_ref);
-        // the row's sum takes the 32-bit probabilities; P V takes them rounded to bf16 (the matrix unit's type)
-        s4[(k >> 1) & 3] += p0 + p1;
-        const __nv_bfloat162 p2 = __floats2bfloat162_rn(p0, p1);
-        pk[k / 2] = *reinterpret_cast<const uint32_t*>(&p2);
-      }
-      l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-      if (i >= PA_NP && ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i / PA_NP) - 1) & 1));
-      // O changes its reference only when a maximum grew by more than 2^8 (no product is running then)
-      if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[(i - 1) % PA_NP], ((i - 1) / PA_NP) & 1));
+      // whether this thread's row is one of the span's
+      const int64_t gr = static_cast<int64_t>(c.t) * PA_ROWS + trow;
+      const bool live = gr < a.BH && (!a.multi || c.b < 0 || (gr >= static_cast<int64_t>(c.b) * a.H &&
+                                                              gr < static_cast<int64_t>(c.b + 1) * a.H));
+      const int len = live ? c.len - 64 * kh - 32 * ch : 0;
+      for (end = c.span(i, n); i < end; ++i, ++c.pos) {
+        const int sb = i % PA_NS, pb = i % PA_NP;
+        const int nvalid = len - PA_T * c.pos;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&s_full[sb], (i / PA_NS) & 1));
         tc_fence_after();
-        #pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-          uint32_t o[32];
-          tmem_ld32(tlane + PT_O + 32 * k, o);
-          tmem_ld_wait();
-          #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(tlane + PT_O + 32 * k, o);
+        uint32_t sr[32];
+        tmem_ld32(t_s + sb * PA_KT, sr);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(c_s_empty + 8 * sb);
+        float z[32];
+        #pragma unroll
+        for (int k = 0; k < 32; ++k) z[k] = k < nvalid ? __uint_as_float(sr[k]) * a.scale_log2 : -INFINITY;
+        float m4[4] = {z[0], z[1], z[2], z[3]};
+        #pragma unroll
+        for (int k = 4; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], z[k]);
+        float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // the row's other keys are other warps'
+        mx[256 * (i & 1) + 128 * ch + L] = mt;
+        named_bar_sync(1, 32 * PA_SM_WARPS);
+        mt = row_max(mx + 256 * (i & 1), mt);
+        float alpha = 1.f;
+        if (mt > m_used + PA_RESCALE || (first && mt > m_used)) {
+          alpha = ex2_approx(m_used - mt);  // 0 from -inf
+          m_used = mt;
         }
-        tmem_st_wait();
+        const float m_ref = m_used == -INFINITY ? 0.f : m_used;
+        uint32_t pk[16];
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        #pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float p0 = ex2_approx(z[k] - m_ref), p1 = ex2_approx(z[k + 1] - m_ref);
+          // the row's sum takes the 32-bit probabilities; P V takes them rounded to bf16 (the matrix unit's type)
+          s4[(k >> 1) & 3] += p0 + p1;
+          const __nv_bfloat162 p2 = __floats2bfloat162_rn(p0, p1);
+          pk[k / 2] = *reinterpret_cast<const uint32_t*>(&p2);
+        }
+        l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+        if (i >= PA_NP && ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i / PA_NP) - 1) & 1));
+        // O changes its reference only when a maximum grew by more than 2^8 (no product is running then)
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[(i - 1) % PA_NP], ((i - 1) / PA_NP) & 1));
+          tc_fence_after();
+          #pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tmem_ld32(t_o + 32 * k, o);
+            tmem_ld_wait();
+            #pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(t_o + 32 * k, o);
+          }
+          tmem_st_wait();
+        }
+        unsigned char* prow = p_s + pb * PA_P_BYTES + kh * PA_P_KB + row * 128;
+        #pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(prow + (((4 * ch + e) ^ (row & 7)) << 4)) =
+              make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(c_p_full + 8 * pb);
+        first = false;
       }
-      unsigned char* prow = p_s + pb * PA_P_BYTES + row * 128;
-      #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<uint4*>(prow + (((4 * kh + e) ^ (row & 7)) << 4)) =
-            make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair(c_p_full + 8 * pb);
-      first = false;
-     }
       const int id = c.id(a), left = c.item_cnt(a) - c.item_pos(a);
       if (i < n) {
         c.settle(a);
@@ -523,40 +562,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       }
       // ---- the item's (or this pair's) last block: the partial sums of its rows
       const int pb = (i - 1) % PA_NP;
-      mx[256 + L] = l;
-      named_bar_sync(1, 128);
-      const float lt = l + mx[256 + (L ^ 64)];
+      float* ls = mx + 256 * (i & 1);  // the maxima of the block before the last: read by all
+      ls[128 * ch + L] = l;
+      named_bar_sync(1, 32 * PA_SM_WARPS);
+      // one order of addition for all four threads of a row
+      const float lt = (ls[row] + ls[128 + row]) + (ls[64 + row] + ls[192 + row]);
       if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i - 1) / PA_NP) & 1));
       tc_fence_after();
       const int64_t prow_i = static_cast<int64_t>(id + pair) * PA_ROWS + trow;
-      // through the warp's quarter of the P buffers (every product is done), 32 rows x 32 columns at a time: a store
-      // instruction writes four whole 128-byte lines in place of 32 rows' 16 bytes (10.7k -> 6.2k clocks a tile)
-      unsigned char* stage = p_s + (warp - PA_SM_WARP) * 4096;
+      // through the warp's part of the P buffers (every product is done), 32 rows x 32 columns at a time: a store
+      // instruction writes four whole 128-byte lines in place of 32 rows' 16 bytes
+      unsigned char* stage = p_s + (warp - PA_SM_WARP) * 2048;
       const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
       const int64_t wrow = prow_i - lane;  // the warp's first row
       #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
-        uint32_t o[32];
-        tmem_ld32(tlane + PT_O + 32 * k, o);
+        uint32_t o[16];
+        tmem_ld16(t_o + 16 * k, o);
         tmem_ld_wait();
         #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         __syncwarp();
         #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = 4 * e + (lane >> 3);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        for (int e = 0; e < 4; ++e) {
+          const int r = 8 * e + (lane >> 2);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
           if ((live_rows >> r) & 1)
-            *reinterpret_cast<uint4*>(a.ws_o + (wrow + r) * 512 + 256 * kh + 32 * k + 4 * (lane & 7)) = v;
+            *reinterpret_cast<uint4*>(a.ws_o + (wrow + r) * 512 + 256 * kh + 128 * ch + 16 * k + 4 * (lane & 3)) = v;
         }
         __syncwarp();
       }
       tc_fence_before();
-      named_bar_sync(1, 128);  // the next block's probabilities go to the same buffers
-      if (live && kh == 0) a.ws_ml[prow_i] = make_float2(m_used, lt);
-      if (rank == 0 && L == 0) {
+      named_bar_sync(1, 32 * PA_SM_WARPS);  // the next block's probabilities go to the same buffers
+      if (live && kh == 0 && ch == 0) a.ws_ml[prow_i] = make_float2(m_used, lt);
+      if (rank == 0 && ch == 0 && L == 0) {
         if (seg_pos == 0) a.seg[id].x = pair;
         if (left == 0) a.seg[id].y = pair;
       }
@@ -681,7 +722,32 @@ __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint
 
 }  // namespace
 
-int make_map(CUtensorMap* m, const void* ptr, bool fp8, int64_t rows, int64_t cols, int box_cols, int box_rows);
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encoder();
+
+// Latent rows as [9 parts of 64 dims][rows][64 dims]: a box of `parts` x box_rows x 64 lands as that many operands of
+// 128-byte rows one behind another (128-byte swizzle), by one instruction.
+static int make_map_parts(CUtensorMap* m, const void* ptr, int64_t rows, int box_rows, int parts) {
+  EncodeTiledFn fn = encoder();
+  if (!fn) {
+    set_last_error("cuTensorMapEncodeTiled unavailable");
+    return LSA_ERR_CUDA;
+  }
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 9};
+  cuuint64_t strides[2] = {1152, 128};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(parts)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_last_error("cuTensorMapEncodeTiled failed");
+    return LSA_ERR_CUDA;
+  }
+  return LSA_OK;
+}
 
 // Scratch: seg int2 [items] | (max, sum) [slots][128] | O [slots][128][512] fp32, slots = items + 74.
 struct PrefixLayout {
@@ -714,7 +780,8 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   a.table_ld = table_ld;
   a.page_shift = 0;
   while ((1 << a.page_shift) < page) ++a.page_shift;
-  a.box = page < 32 ? page : 32;
+  a.kbox = page < PA_KT ? page : PA_KT;
+  a.vbox = page < PA_VT ? page : PA_VT;
   a.n_pages = static_cast<int>(n_pages);
   a.cap = static_cast<int>(table_ld * page < 0x7FFFFF00 ? table_ld * page : 0x7FFFFF00);
   a.B = static_cast<int>(B);
@@ -729,15 +796,18 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   a.ws_ml = reinterpret_cast<float2*>(base + p.o_ml);
   a.ws_o = reinterpret_cast<float*>(base + p.o_o);
   // an absent part's maps cover the queries: nothing is loaded through them
-  CUtensorMap tq, tk, tv, tp;
-  int st = make_map(&tq, q, false, a.BH, 576, 64, 64);
-  if (st == LSA_OK) st = Lp > 0 ? make_map(&tk, prefix, false, Lp, 576, 64, PA_T / 2) : make_map(&tk, q, false, a.BH, 576, 64, 32);
-  if (st == LSA_OK) st = Lp > 0 ? make_map(&tv, prefix, false, Lp, 576, 64, PA_T) : make_map(&tv, q, false, a.BH, 576, 64, 32);
+  CUtensorMap tq, tk, tv, tpk, tpv;
+  const int64_t own_rows = n_pages * page;
+  int st = make_map_parts(&tq, q, a.BH, 64, 9);
+  if (st == LSA_OK) st = make_map_parts(&tk, Lp > 0 ? prefix : q, Lp > 0 ? Lp : a.BH, PA_KT, PA_KS);
+  if (st == LSA_OK) st = make_map_parts(&tv, Lp > 0 ? prefix : q, Lp > 0 ? Lp : a.BH, PA_VT, 4);
   if (st == LSA_OK)
-    st = n_pages > 0 ? make_map(&tp, pages, false, n_pages * page, 576, 64, a.box) : make_map(&tp, q, false, a.BH, 576, 64, 32);
+    st = make_map_parts(&tpk, own_rows > 0 ? pages : q, own_rows > 0 ? own_rows : a.BH, a.kbox, a.kbox == PA_KT ? PA_KS : 1);
+  if (st == LSA_OK)
+    st = make_map_parts(&tpv, own_rows > 0 ? pages : q, own_rows > 0 ? own_rows : a.BH, a.vbox, a.vbox == PA_VT ? 4 : 1);
   if (st != LSA_OK) return st;
   LSA_CUDA_TRY(func_smem_once(reinterpret_cast<const void*>(k_prefix_attn), PA_SMEM));
-  LSA_CUDA_TRY(launch_pdl(k_prefix_attn, dim3(2 * PA_PAIRS), dim3(PA_THREADS), PA_SMEM, s, 0u, tq, tk, tv, tp, a));
+  LSA_CUDA_TRY(launch_pdl(k_prefix_attn, dim3(2 * PA_PAIRS), dim3(PA_THREADS), PA_SMEM, s, 0u, tq, tk, tv, tpk, tpv, a));
   // a row has about 74 / tiles partials
   const dim3 rows(static_cast<unsigned>(a.BH));
   return cuda_status(a.nT <= 8 ? launch_pdl(k_prefix_combine<4>, rows, dim3(512), 0, s, 0u, a, static_cast<uint16_t*>(out), lse)

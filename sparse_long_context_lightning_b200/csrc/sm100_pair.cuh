@@ -57,6 +57,14 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t cbar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(cbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // Arrive on a barrier of either CTA of the pair (shared::cluster address).  The release is at CTA scope: what it publishes
 // is this CTA's own tensor memory (loaded to registers before) and its own shared memory (written, then fenced for the
 // async proxy), and the matrix instructions that follow read them where they lie.  A release at cluster scope also
