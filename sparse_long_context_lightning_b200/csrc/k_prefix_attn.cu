@@ -16,8 +16,8 @@
 // twice, 1088 bytes a key and CTA, the second time from L2.  Keys arrive in stages of 64 keys x 192 dims (three a
 // block) and values in stages of 32 keys, each by one instruction of a three-dimensional map: a warp that issues a load
 // waits about 200 clocks before its next, so nine small loads a block held the block at 3750 clocks.  With 64-key
-// blocks (N = 64, A read again for each, 22.6 clocks a key and SM against 17.0) the same batch took 529 us against 470.
-// 16 queries of 128 heads behind 131072 rows: 470 us, 1240 TFLOP/s; 64 queries behind 32749: 414 us, 1430 TFLOP/s,
+// blocks (N = 64, A read again for each, 22.6 clocks a key and SM against 17.0) the same batch took 529 us against 470 (before the walk below).
+// 16 queries of 128 heads behind 131072 rows: 398 us, 1470 TFLOP/s; 64 queries behind 32749: 399 us, 1485 TFLOP/s,
 // where the GPU's power limit holds the clock near 1.4 GHz (cuBLAS sustains 1385 there).
 //
 // Work is cut evenly: the blocks of all tiles, in order, are one line that 74 pairs divide; a tile that spans pairs
@@ -91,6 +91,7 @@ struct Cursor {
   int t, b;  // tile; query whose own blocks are walked, or -1: the prefix
   int pos, cnt;
   int len;  // keys of the prefix or of the query's pages
+  int turn, wrap, width;  // of the span: where the walk begins
   int qlo, qhi;
 
   static __device__ __forceinline__ int len_of(const PaArgs& a, int b) {
@@ -127,8 +128,29 @@ struct Cursor {
     pos = off;
     settle(a);
   }
-  // the span's end among the pair's n blocks, of which i are done
-  __device__ __forceinline__ int span(int i, int n) const { return min(n, cnt - pos > n - i ? n : i + cnt - pos); }
+  // The span's end among the pair's n blocks, of which i are done.  A prefix span is walked from the block that is i
+  // modulo n, and round: pairs at the same i then read the same few places of the prefix whichever tile they work on, so
+  // that a prefix larger than the L2 comes from HBM about once (n differs by one block between pairs at most): 16 queries
+  // of 128 heads behind 131072 rows (151 MB) 458 -> 398 us.
+  __device__ __forceinline__ int span(int i, int n) {
+    const int w = min(n - i, cnt - pos);
+    turn = 0;
+    wrap = 0x7FFFFFFF;
+    width = w;
+    if (b < 0) {
+      int r = (i - pos) % n;
+      if (r < 0) r += n;
+      if (r < w) {
+        turn = r;
+        wrap = pos + w;
+      }
+    }
+    return i + w;
+  }
+  __device__ __forceinline__ int block() const {
+    const int x = pos + turn;
+    return x >= wrap ? x - width : x;
+  }
   __device__ __forceinline__ int id(const PaArgs& a) const {
     return !a.multi ? t : (b < 0 ? qlo + 2 * t : b + 2 * t + 1);
   }
@@ -263,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     uint32_t s = 0, phase = 1;
     for (int i = 0, end; i < n && ok;) {
       for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
-        const int key0 = PA_T * c.pos + PA_KT * static_cast<int>(rank);
+        const int key0 = PA_T * c.block() + PA_KT * static_cast<int>(rank);
         // page rows of this CTA's keys (lane = box); a box past the end reads as zeros: a row outside the map
         int y = PA_NO_ROW;
         if (c.b >= 0) {
@@ -321,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     uint32_t s = 0, phase = 1;
     for (int i = 0, end; i < n && ok;) {
       for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
-        const int key0 = PA_T * c.pos;
+        const int key0 = PA_T * c.block();
         int y = PA_NO_ROW;
         if (c.b >= 0) {
           const int key = key0 + lane * a.vbox;
@@ -440,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           ok = mbar_wait_cluster(&p_full[pb], (i / PA_NP) & 1);
           #pragma unroll
           for (int k = 0; k < PA_T / PA_VT; ++k) {
-            if (PA_T * c.pos + PA_VT * k >= c.len) break;
+            if (PA_T * c.block() + PA_VT * k >= c.len) break;
             ok = ok && mbar_wait_cluster(&v_full[s], phase);
             if (!ok) break;
             tc_fence_after();
@@ -491,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       const int len = live ? c.len - 64 * kh - 32 * ch : 0;
       for (end = c.span(i, n); i < end; ++i, ++c.pos) {
         const int sb = i % PA_NS, pb = i % PA_NP;
-        const int nvalid = len - PA_T * c.pos;
+        const int nvalid = len - PA_T * c.block();
         if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&s_full[sb], (i / PA_NS) & 1));
         tc_fence_after();
         uint32_t sr[32];
