@@ -104,9 +104,9 @@ struct Cursor {
     b = -1;
     cnt = a.nP;
     len = static_cast<int>(a.Lp);
-    const int64_t r0 = static_cast<int64_t>(tt) * PA_ROWS;
-    qlo = static_cast<int>(r0 / a.H);
-    qhi = static_cast<int>(min(r0 + PA_ROWS, a.BH) - 1) / a.H;
+    const uint32_t r0 = static_cast<uint32_t>(tt) * PA_ROWS, h = static_cast<uint32_t>(a.H);  // rows fit 31 bits
+    qlo = static_cast<int>(r0 / h);
+    qhi = static_cast<int>((min(r0 + PA_ROWS, static_cast<uint32_t>(a.BH)) - 1) / h);
   }
   __device__ __forceinline__ void settle(const PaArgs& a) {  // to the block that `pos` counts up to; one must be left
     while (pos >= cnt) {
@@ -162,8 +162,10 @@ __device__ __forceinline__ int tile_blocks(const PaArgs& a, int t) {
   Cursor c;
   c.tile(a, t);
   int n = a.nP;
-  if (a.own_len)
+  if (a.own_len) {
+    #pragma unroll 4
     for (int b = c.qlo; b <= c.qhi; ++b) n += Cursor::blocks_of(a, b);
+  }
   return n;
 }
 
@@ -178,7 +180,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   unsigned char* v_s = k_s + PA_NK * PA_K_BYTES;
   float* mx = reinterpret_cast<float*>(v_s + PA_NV * PA_V_BYTES);  // [2][256]: row maxima of a block, row sums
   uint64_t* q_full = reinterpret_cast<uint64_t*>(mx + 2 * 256);
-  uint64_t* q_empty = q_full + 1;
+  uint64_t* q_empty = q_full + 3;
   uint64_t* k_full = q_empty + 1;
   uint64_t* k_empty = k_full + PA_NK;
   uint64_t* v_full = k_empty + PA_NK;
@@ -198,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1);
 
   if (tid == 0) {
-    mbar_init(q_full, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&q_full[i], 1);
     mbar_init(q_empty, 1);
     for (int i = 0; i < PA_NK; ++i) {
       mbar_init(&k_full[i], 1);
@@ -225,6 +227,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     tma_prefetch_desc(&tm_v);
   }
   if (warp == PA_PV_WARP) tmem_alloc_pair(tmem_holder, 512);
+  tc_fence_before();
+  cluster_sync_all();  // the barriers and the tensor memory of both CTAs are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
   // every global access of this kernel comes after the previous kernel of the stream has completed
   pdl_wait();
   pdl_launch_dependents();
@@ -250,9 +256,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       if (w < warp) before += sums[w];
       total += sums[w];
     }
-    const int64_t np = min(static_cast<int64_t>(PA_PAIRS), total);
+    const int np = static_cast<int>(min(static_cast<int64_t>(PA_PAIRS), total));
     if (pair < np) {
-      const int64_t s0 = total * pair / np, s1 = total * (pair + 1) / np;
+      int64_t s0, s1;
+      if (total < (1 << 24)) {  // a 64-bit division takes as long as a load
+        s0 = static_cast<uint32_t>(total) * pair / np;
+        s1 = static_cast<uint32_t>(total) * (pair + 1) / np;
+      } else {
+        s0 = total * pair / np;
+        s1 = total * (pair + 1) / np;
+      }
       if (s0 >= before && s0 < before + mine) {
         int64_t off = s0 - before;
         int t = lo;
@@ -269,11 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       for (int b = tid; b < a.B; b += PA_THREADS)
         if (a.own_len[b] < 0 || a.own_len[b] > a.cap) atomicExch(&g_prefix_check, 1);
   }
-  tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the barriers and the tensor memory of both CTAs are there
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
   const int n = start_s[2];
   Cursor c;
   if (n > 0) c.start(a, start_s[0], start_s[1]);
@@ -296,14 +305,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           }
         }
         const bool one = elect_one();
-        if (c.t != loaded) {
+        const bool fresh = c.t != loaded;
+        if (fresh) {
           ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1));
-          if (ok && one) {
-            if (rank == 0) mbar_expect_tx(q_full, 2 * PA_Q_BYTES);
-            const uint32_t bar = mapa(smem_u32(q_full), 0);
-            tma_load_3d_pair(q_s, &tm_q, bar, 0, c.t * PA_ROWS + 64 * static_cast<int>(rank), 0);
-          }
-          __syncwarp();
+          if (!ok) break;
           loaded = c.t;
           ++nq;
         }
@@ -312,6 +317,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           if (!ok) break;
           const uint32_t bar = mapa(smem_u32(&k_full[s]), 0);
           unsigned char* dst = k_s + s * PA_K_BYTES;
+          if (fresh && one) {  // the tile's queries arrive in the same parts as its first keys
+            if (rank == 0) mbar_expect_tx(&q_full[j / PA_KS], 2 * PA_KS * PA_Q_KB);
+            tma_load_3d_pair(q_s + j * PA_Q_KB, &tm_q, mapa(smem_u32(&q_full[j / PA_KS]), 0), 0,
+                             c.t * PA_ROWS + 64 * static_cast<int>(rank), j);
+          }
           if (one && rank == 0) mbar_expect_tx(&k_full[s], 2 * PA_K_BYTES);
           if (c.b < 0) {
             if (one) tma_load_3d_pair(dst, &tm_k, bar, 0, key0, j);
@@ -421,11 +431,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       for (int i = 0, end; i < n && ok;) {
         for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
           const int sb = i % PA_NS;
-          if (fresh) ok = mbar_wait_cluster(q_full, nq++ & 1);
-          fresh = false;
           ok = ok && mbar_wait_cluster(&s_empty[sb], ((i / PA_NS) & 1) ^ 1);
           #pragma unroll
           for (int kb = 0; kb < 9; kb += PA_KS) {
+            if (fresh) ok = ok && mbar_wait_cluster(&q_full[kb / PA_KS], nq & 1);
             ok = ok && mbar_wait_cluster(&k_full[s], phase);
             if (!ok) break;
             tc_fence_after();
@@ -440,6 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
             }
           }
           if (ok) mma_commit_pair(&s_full[sb]);
+          if (fresh) ++nq;
+          fresh = false;
         }
         if (i >= n || !ok) break;
         const int t = c.t;
@@ -598,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
       const int64_t wrow = prow_i - lane;  // the warp's first row
       #pragma unroll 1
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 8 && live_rows != 0; ++k) {
         uint32_t o[16];
         tmem_ld16(t_o + 16 * k, o);
         tmem_ld_wait();
@@ -653,52 +664,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
 template <int G>
 __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint16_t* __restrict__ out,
                                                             float* __restrict__ lse) {
-  constexpr int MAXP = 2 * PA_PAIRS;
+  constexpr int MAXP = 2 * PA_PAIRS, U = 6;
   __shared__ float wt[MAXP];
   __shared__ float4 acc_s[G > 1 ? (G - 1) * 128 : 1];
   __shared__ float red[2 * 4 * G];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t r = blockIdx.x;
-  const int b = static_cast<int>(r / a.H), t = static_cast<int>(r / PA_ROWS), tr = static_cast<int>(r % PA_ROWS);
+  const uint32_t ur = static_cast<uint32_t>(r), uh = static_cast<uint32_t>(a.H);
+  const int b = static_cast<int>(ur / uh), t = static_cast<int>(ur / PA_ROWS), tr = static_cast<int>(ur % PA_ROWS);
+  const int qlo = static_cast<int>(static_cast<uint32_t>(t) * PA_ROWS / uh);
+  // the row's items (the first and the last pair of each; written for items that have blocks, so the loads need not
+  // wait for the length) and the number of their partials
+  const int i0 = a.multi ? qlo + 2 * t : t, i1 = a.multi ? b + 2 * t + 1 : t;
+  const int2 g0 = a.seg[i0], g1 = a.seg[i1];
   const int ob = Cursor::blocks_of(a, b);
-  int id[2], n[2];  // the row's items: its first slot, number of slots
-  int2 sg = make_int2(0, -1);
-  if (!a.multi) {
-    if (a.nP + ob > 0) sg = a.seg[t];
-    id[0] = t + sg.x;
-    n[0] = sg.y - sg.x + 1;
-    id[1] = n[1] = 0;
-  } else {
-    const int qlo = static_cast<int>(static_cast<int64_t>(t) * PA_ROWS / a.H);
-    int2 sh = make_int2(0, -1);
-    if (a.nP > 0) sg = a.seg[qlo + 2 * t];
-    if (ob > 0) sh = a.seg[b + 2 * t + 1];
-    id[0] = qlo + 2 * t + sg.x;
-    n[0] = sg.y - sg.x + 1;
-    id[1] = b + 2 * t + 1 + sh.x;
-    n[1] = sh.y - sh.x + 1;
+  const int n0 = (a.multi ? a.nP : a.nP + ob) > 0 ? g0.y - g0.x + 1 : 0;
+  const int n1 = a.multi && ob > 0 ? g1.y - g1.x + 1 : 0;
+  const int parts = min(max(n0, 0) + max(n1, 0), MAXP);
+  auto slot_row = [&](int i) { return static_cast<int64_t>(i < n0 ? i0 + g0.x + i : i1 + g1.x + i - n0) * PA_ROWS + tr; };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = tid & 127;
+  // the maxima and sums of the parts tid and tid + 128 G, and the first of the values on their way at the same time
+  constexpr int ML = G > 1 ? 1 : 2;
+  float2 ml[ML];
+  #pragma unroll
+  for (int k = 0; k < ML; ++k) {
+    const int i = tid + 128 * G * k;
+    ml[k] = i < parts ? a.ws_ml[slot_row(i)] : make_float2(0.f, 0.f);
   }
-  const int parts = min(n[0] + n[1], MAXP);
-  auto slot_row = [&](int i) { return static_cast<int64_t>(i < n[0] ? id[0] + i : id[1] + i - n[0]) * PA_ROWS + tr; };
-  // the parts' maxima and sums: part tid (and tid + 128 G where there are that many)
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float4 v[U];
+  #pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int i = (tid >> 7) + G * k;
+    v[k] = i < parts ? reinterpret_cast<const float4*>(a.ws_o + slot_row(i) * 512)[col] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   float m = -INFINITY;
-  for (int i = tid; i < parts; i += 128 * G) {
-    const float2 ml = a.ws_ml[slot_row(i)];
-    if (ml.y != 0.f) m = fmaxf(m, ml.x);
-  }
+  #pragma unroll
+  for (int k = 0; k < ML; ++k)
+    if (ml[k].y != 0.f) m = fmaxf(m, ml[k].x);
   m = warp_max(m);
   if (lane == 0) red[warp] = m;
   __syncthreads();
   #pragma unroll
   for (int w = 0; w < 4 * G; ++w) m = fmaxf(m, red[w]);
   float l = 0.f;
-  for (int i = tid; i < parts; i += 128 * G) {
-    const float2 ml = a.ws_ml[slot_row(i)];
-    const float w = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
-    wt[i] = w;
-    l += w * ml.y;
+  #pragma unroll
+  for (int k = 0; k < ML; ++k) {
+    const int i = tid + 128 * G * k;
+    const float w = ml[k].y != 0.f ? exp2f(ml[k].x - m) : 0.f;
+    if (i < parts) wt[i] = w;
+    l += w * ml[k].y;
   }
   l = warp_sum(l);
   if (lane == 0) red[4 * G + warp] = l;
@@ -706,17 +721,25 @@ __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint
   l = 0.f;
   #pragma unroll
   for (int w = 0; w < 4 * G; ++w) l += red[4 * G + w];
-  const int col = tid & 127;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  #pragma unroll 4
-  for (int i = tid >> 7; i < parts; i += G) {
-    const float w = wt[i];
-    const float4 v = reinterpret_cast<const float4*>(a.ws_o + slot_row(i) * 512)[col];
-    if (w != 0.f) {  // a partial without keys holds nothing
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
+  for (int i0k = tid >> 7; i0k < parts; i0k += G * U) {
+    float4 nx[U];
+    #pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0k + G * (U + k);
+      nx[k] = i < parts ? reinterpret_cast<const float4*>(a.ws_o + slot_row(i) * 512)[col] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    #pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0k + G * k;
+      const float w = i < parts ? wt[i] : 0.f;
+      if (w != 0.f) {  // a partial without keys holds nothing
+        acc.x += w * v[k].x;
+        acc.y += w * v[k].y;
+        acc.z += w * v[k].z;
+        acc.w += w * v[k].w;
+      }
+      v[k] = nx[k];
     }
   }
   if (G > 1) {
@@ -820,7 +843,7 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   // an absent part's maps cover the queries: nothing is loaded through them
   CUtensorMap tq, tk, tv, tpk, tpv;
   const int64_t own_rows = n_pages * page;
-  int st = make_map_parts(&tq, q, a.BH, 64, 9);
+  int st = make_map_parts(&tq, q, a.BH, 64, PA_KS);
   if (st == LSA_OK) st = make_map_parts(&tk, Lp > 0 ? prefix : q, Lp > 0 ? Lp : a.BH, PA_KT, PA_KS);
   if (st == LSA_OK) st = make_map_parts(&tv, Lp > 0 ? prefix : q, Lp > 0 ? Lp : a.BH, PA_VT, 4);
   if (st == LSA_OK)
