@@ -8,7 +8,6 @@ the first call does, and raises ``LsaError`` if the built library is missing.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -311,40 +310,38 @@ def lsa_msa_attn(q, kv, idx, gmask, count, G, scale, out, lse=None, ws=None, str
     _check("lsa_msa_attn", st)
 
 
-def _need(fn: str, ok: bool, what: str):
-    if not ok:
-        raise LsaError(fn, -1, what)
+# The calls below take a few microseconds on the GPU in a decode step, so their checks are written to cost little: one test
+# a tensor, messages formed on failure only, the stream asked for as a number (a Stream object costs 3 us).
 
 
-def _vec(fn: str, name: str, t, dtype, shape, device):
-    """Address of an optional contiguous tensor of this dtype, shape and device."""
+def _bad(fn: str, what: str):
+    raise LsaError(fn, -1, what)
+
+
+def _vec(fn: str, name: str, t, dtype, shape, dev: int):
+    """Address of an optional contiguous tensor of this dtype and shape on GPU `dev`."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise LsaError(fn, -1, f"{name}: contiguous {dtype} {tuple(shape)} on {device} wanted, got {t.dtype} "
-                               f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise LsaError(fn, -1, f"{name}: contiguous {dtype} {tuple(shape)} on cuda:{dev} wanted, got {t.dtype} "
+                           f"{tuple(t.shape)} on {t.device}")
 
 
 def _code(fn: str, name: str, table: dict, key) -> int:
-    if key not in table:
-        raise LsaError(fn, -1, f"{name} must be one of {', '.join(table)}, got {key!r}")
-    return table[key]
+    c = table.get(key)
+    if c is None:
+        _bad(fn, f"{name} must be one of {', '.join(table)}, got {key!r}")
+    return c
 
 
-_same_device = contextlib.nullcontext()
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _on(t):
-    """The tensors' GPU as the current one for the call (its stream, its kernels)."""
-    return _same_device if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-
-def _strides(fn: str, name: str, t):
-    """Token and head strides of [T, H, D] in elements; an axis of length one has none that matters."""
-    st, sh, sd = t.stride()
-    _need(fn, sd == 1 or t.shape[2] == 1, f"{name}: the last axis must be contiguous")
-    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+def _off_device(t) -> bool:
+    """Whether the call has to make the tensors' GPU the current one first."""
+    return t.get_device() != torch._C._cuda_getDevice()
 
 
 def lsa_rope_freqs(R, base=10000.0, scaling="none", factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0,
@@ -363,30 +360,49 @@ def lsa_norm_rope(x, y, pos=None, freqs=None, norm="none", weight=None, bias=Non
     """y[t, h] = norm of x[t, h] with dims [rope_off, rope_off + 2 len(freqs)) rotated by pos[t]; x bf16 [T, H, D] with
     any token and head strides, y bf16 (it may be x) or, with y_scale [T, H], e4m3 codes."""
     fn = "lsa_norm_rope"
-    _need(fn, x.dim() == 3 and x.is_cuda and x.dtype == torch.bfloat16, "x: bf16 [T, H, D] on a GPU wanted")
-    _need(fn, y.shape == x.shape and y.device == x.device, "y: the shape and device of x wanted")
-    T, H, D = x.shape
-    dtype, dev, f32 = _dtype_code(y), x.device, torch.float32
-    xt, xh = _strides(fn, "x", x)
-    yt, yh = _strides(fn, "y", y)
-    _need(fn, (T == 1 or yt) and (H == 1 or yh), "y: a broadcast output")
-    _need(fn, pos is None or freqs is not None, "pos without freqs")
-    _need(fn, freqs is None or pos is not None, "freqs without pos")
-    with _on(x):
-        st = load_library().lsa_norm_rope(
-            x.data_ptr(), xt, xh, T, H, D, _code(fn, "norm", _NORMS, norm),
-            _vec(fn, "weight", weight, f32, (D,), dev), _vec(fn, "bias", bias, f32, (D,), dev), eps,
-            None if freqs is None else _vec(fn, "freqs", freqs, torch.float64, freqs.shape[:1], dev), rope_off,
-            0 if freqs is None else 2 * freqs.shape[0], _code(fn, "layout", _LAYOUTS, layout), mul,
-            _vec(fn, "pos", pos, torch.int64, (T,), dev), y.data_ptr(), yt, yh, dtype,
-            _vec(fn, "y_scale", y_scale, f32, (T, H), dev), _stream(stream))
-    _check(fn, st)
+    if x.dim() != 3 or not x.is_cuda or x.dtype is not torch.bfloat16:
+        _bad(fn, "x: bf16 [T, H, D] on a GPU wanted")
+    if _off_device(x):
+        with torch.cuda.device(x.device):
+            return lsa_norm_rope(x, y, pos, freqs, norm, weight, bias, eps, rope_off, layout, mul, y_scale, stream)
+    T, H, D = shape = x.shape
+    dev, f32 = x.get_device(), torch.float32
+    if y.shape != shape or y.get_device() != dev:
+        _bad(fn, "y: the shape and device of x wanted")
+    (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
+    if (xd != 1 or yd != 1) and D != 1:
+        _bad(fn, "x, y: the last axis must be contiguous")
+    if T == 1:  # an axis of length one has no stride that matters
+        xt = yt = 0
+    elif yt == 0:
+        _bad(fn, "y: a broadcast output")
+    if H == 1:
+        xh = yh = 0
+    elif yh == 0:
+        _bad(fn, "y: a broadcast output")
+    R = 0
+    if freqs is not None:
+        if pos is None or freqs.dim() != 1:
+            _bad(fn, "freqs [rotary dims / 2] and pos belong together")
+        R = 2 * freqs.shape[0]
+    elif pos is not None:
+        _bad(fn, "pos without freqs")
+    st = load_library().lsa_norm_rope(
+        x.data_ptr(), xt, xh, T, H, D, _code(fn, "norm", _NORMS, norm), _vec(fn, "weight", weight, f32, (D,), dev),
+        _vec(fn, "bias", bias, f32, (D,), dev), eps, _vec(fn, "freqs", freqs, torch.float64, (R // 2,), dev), rope_off, R,
+        _code(fn, "layout", _LAYOUTS, layout), mul, _vec(fn, "pos", pos, torch.int64, (T,), dev), y.data_ptr(), yt, yh,
+        _dtype_code(y), _vec(fn, "y_scale", y_scale, f32, (T, H), dev), _raw_stream(stream, dev))
+    if st:
+        _check(fn, st)
 
 
-def _rows(fn: str, name: str, t, T, D, device):
-    ok = t.shape == (T, D) and t.dtype == torch.bfloat16 and t.device == device and t.stride(1) == 1
-    _need(fn, ok, f"{name}: bf16 [{T}, {D}] on {device} with contiguous rows wanted")
-    return t.stride(0) if T > 1 else 0
+def _rows(fn: str, name: str, t, T, D, dev: int) -> int:
+    """Row stride of bf16 [T, D] with contiguous rows."""
+    if t.shape == (T, D) and t.dtype is torch.bfloat16 and t.get_device() == dev:
+        st, sd = t.stride()
+        if sd == 1:
+            return st if T > 1 else 0
+    raise LsaError(fn, -1, f"{name}: bf16 [{T}, {D}] on cuda:{dev} with contiguous rows wanted")
 
 
 def lsa_cache_append(a, kv, slot, pos=None, freqs=None, kv_weight=None, kv_eps=1e-6, layout="interleaved", mul=1.0,
@@ -395,29 +411,36 @@ def lsa_cache_append(a, kv, slot, pos=None, freqs=None, kv_weight=None, kv_eps=1
     """kv[slot[t]] = a[t] with its first 512 dims RMS-normed (kv_weight given) and its last 64 rotated by pos[t]; with k,
     the index keys normed, rotated and written to k_cache[slot[t]] too (bf16, or e4m3 codes with k_scale)."""
     fn = "lsa_cache_append"
-    dev, f32, i64 = a.device, torch.float32, torch.int64
-    T = slot.shape[0]
-    _need(fn, a.is_cuda, "tensors on a GPU wanted")
+    if not a.is_cuda or slot.dim() != 1 or kv.dim() != 2:
+        _bad(fn, "a [T, 576], kv [slots, 576] and slot [T] on a GPU wanted")
+    if _off_device(a):
+        with torch.cuda.device(a.device):
+            return lsa_cache_append(a, kv, slot, pos, freqs, kv_weight, kv_eps, layout, mul, k, k_cache, k_scale, k_norm,
+                                    k_weight, k_bias, k_eps, k_rope_off, k_layout, stream)
+    dev, f32, bf = a.get_device(), torch.float32, torch.bfloat16
+    T, n = slot.shape[0], kv.shape[0]
+    if (freqs is None) != (pos is None) or (k is None) != (k_cache is None):
+        _bad(fn, "freqs and pos, and k and k_cache, belong together")
     a_ld = _rows(fn, "a", a, T, 576, dev)
-    n = kv.shape[0]
-    _need(fn, (freqs is None) == (pos is None), "freqs and pos belong together")
-    _need(fn, (k is None) == (k_cache is None), "k and k_cache belong together")
-    k_ld = d_I = k_dtype = 0
-    k_cache_p = None
+    k_p, k_ld, d_I, k_dtype, kc_p = None, 0, 0, 0, None
     if k is not None:
+        if k.dim() != 2:
+            _bad(fn, "k [T, d_I] wanted")
         d_I, k_dtype = k.shape[1], _dtype_code(k_cache)
-        k_ld = _rows(fn, "k", k, T, d_I, dev)
-        k_cache_p = _vec(fn, "k_cache", k_cache, k_cache.dtype, (n, d_I), dev)
-    with _on(a):
-        st = load_library().lsa_cache_append(
-            a.data_ptr(), a_ld, T, a.shape[1], 512, _vec(fn, "kv_weight", kv_weight, f32, (512,), dev), kv_eps,
-            _vec(fn, "freqs", freqs, torch.float64, (32,), dev), _code(fn, "layout", _LAYOUTS, layout), mul,
-            _vec(fn, "pos", pos, i64, (T,), dev), _vec(fn, "slot", slot, i64, (T,), dev),
-            _vec(fn, "kv", kv, torch.bfloat16, (n, 576), dev), n, _ptr(k), k_ld, d_I, _code(fn, "k_norm", _NORMS, k_norm),
-            _vec(fn, "k_weight", k_weight, f32, (d_I,), dev), _vec(fn, "k_bias", k_bias, f32, (d_I,), dev), k_eps,
-            k_rope_off if k is not None else -1, _code(fn, "k_layout", _LAYOUTS, k_layout), k_cache_p, k_dtype,
-            _vec(fn, "k_scale", k_scale, f32, (n,), dev), _stream(stream))
-    _check(fn, st)
+        k_p, k_ld = k.data_ptr(), _rows(fn, "k", k, T, d_I, dev)
+        kc_p = _vec(fn, "k_cache", k_cache, k_cache.dtype, (n, d_I), dev)
+    else:
+        k_rope_off = -1
+    st = load_library().lsa_cache_append(
+        a.data_ptr(), a_ld, T, 576, 512, _vec(fn, "kv_weight", kv_weight, f32, (512,), dev), kv_eps,
+        _vec(fn, "freqs", freqs, torch.float64, (32,), dev), _code(fn, "layout", _LAYOUTS, layout), mul,
+        _vec(fn, "pos", pos, torch.int64, (T,), dev), _vec(fn, "slot", slot, torch.int64, (T,), dev),
+        _vec(fn, "kv", kv, bf, (n, 576), dev), n, k_p, k_ld, d_I, _code(fn, "k_norm", _NORMS, k_norm),
+        _vec(fn, "k_weight", k_weight, f32, (d_I,), dev), _vec(fn, "k_bias", k_bias, f32, (d_I,), dev), k_eps, k_rope_off,
+        _code(fn, "k_layout", _LAYOUTS, k_layout), kc_p, k_dtype, _vec(fn, "k_scale", k_scale, f32, (n,), dev),
+        _raw_stream(stream, dev))
+    if st:
+        _check(fn, st)
 
 
 def lsa_prefix_attn_workspace_size(B, H):
@@ -428,24 +451,36 @@ def lsa_prefix_attn(q, prefix, scale, out, lse=None, pages=None, table=None, own
     """out[b, h] = softmax over the rows of `prefix` (None: no prefix) and the query's own own_len[b] rows in `pages`
     ([n_pages, page, 576], found through table [B, cols]) of scale q.k, times the rows' first 512 dims."""
     fn = "lsa_prefix_attn"
-    _need(fn, q.dim() == 3 and q.is_cuda, "q: bf16 [B, H, 576] on a GPU wanted")
+    if q.dim() != 3 or not q.is_cuda or out.dim() != 3:
+        _bad(fn, "q [B, H, 576] and out [B, H, 512] on a GPU wanted")
+    if _off_device(q):
+        with torch.cuda.device(q.device):
+            return lsa_prefix_attn(q, prefix, scale, out, lse, pages, table, own_len, ws, stream)
+    dev, bf, i32 = q.get_device(), torch.bfloat16, torch.int32
     B, H, d_qk = q.shape
-    dev, bf, i32 = q.device, torch.bfloat16, torch.int32
-    d_v, Lp, n_pages, page, cols = out.shape[-1], 0, 0, 0, 0
-    if prefix is not None:
-        Lp = prefix.shape[0]
-    _need(fn, (own_len is None) == (pages is None) == (table is None), "pages, table and own_len belong together")
+    d_v = out.shape[2]
+    Lp = 0 if prefix is None else prefix.shape[0]
+    n_pages = page = cols = 0
     if own_len is not None:
-        _need(fn, pages.dim() == 3 and table.dim() == 2, "pages [n_pages, page, 576] and table [B, cols] wanted")
-        n_pages, page, cols = pages.shape[0], pages.shape[1], table.shape[1]
-    with _on(q):
-        st = load_library().lsa_prefix_attn(
-            _vec(fn, "q", q, bf, q.shape, dev), B, H, d_qk, d_v, _vec(fn, "prefix", prefix, bf, (Lp, d_qk), dev), Lp,
-            _vec(fn, "pages", pages, bf, (n_pages, page, d_qk), dev), n_pages, page,
-            _vec(fn, "table", table, i32, (B, cols), dev), cols, _vec(fn, "own_len", own_len, i32, (B,), dev), scale,
-            _vec(fn, "out", out, bf, (B, H, d_v), dev), _vec(fn, "lse", lse, torch.float32, (B, H), dev), _ptr(ws),
-            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
-    _check(fn, st)
+        if pages is None or table is None or pages.dim() != 3 or table.dim() != 2:
+            _bad(fn, "pages [n_pages, page, 576] and table [B, cols] wanted with own_len")
+        n_pages, page, _ = pages.shape
+        cols = table.shape[1]
+    elif pages is not None or table is not None:
+        _bad(fn, "pages and table without own_len")
+    ws_p = ws_n = 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            _bad(fn, "ws: contiguous bytes on the GPU of q wanted")
+        ws_p, ws_n = ws.data_ptr(), ws.numel() * ws.element_size()
+    st = load_library().lsa_prefix_attn(
+        _vec(fn, "q", q, bf, (B, H, d_qk), dev), B, H, d_qk, d_v, _vec(fn, "prefix", prefix, bf, (Lp, d_qk), dev), Lp,
+        _vec(fn, "pages", pages, bf, (n_pages, page, d_qk), dev), n_pages, page,
+        _vec(fn, "table", table, i32, (B, cols), dev), cols, _vec(fn, "own_len", own_len, i32, (B,), dev), scale,
+        _vec(fn, "out", out, bf, (B, H, d_v), dev), _vec(fn, "lse", lse, torch.float32, (B, H), dev), ws_p, ws_n,
+        _raw_stream(stream, dev))
+    if st:
+        _check(fn, st)
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
