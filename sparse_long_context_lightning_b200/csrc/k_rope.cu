@@ -3,12 +3,12 @@
 //   n = x | x / sqrt(mean x^2 + eps) w | (x - mean x) / sqrt(var x + eps) w + b      (one head row of D dims)
 //   (u, v) -> (u c - v s, v c + u s),  c = mul cos(pos f_i), s = mul sin(pos f_i)     (pairs of dims [off, off + R))
 //
-// The angle pos f_i is formed and reduced modulo 2 pi in 64 bits: a 32-bit angle at position 10^7 is off by half a
-// radian.  What is left, |r| <= pi, goes through sincosf in 32 bits.  Norm statistics are 32-bit sums over the row's
-// registers (the layer norm's variance from the centred values), and each result is rounded once.
+// The angle pos f_i is formed and reduced to a part of a turn in 64 bits: a 32-bit angle at position 10^7 is off by half
+// a radian.  What is left, half a turn at most, goes through sincospif in 32 bits.  Norm statistics are 32-bit sums over
+// the row's registers (the layer norm's variance from the centred values), and each result is rounded once.
 //
-// Both kernels move bytes: 16-byte loads and stores, one row per group of lanes, so a row's sums are shuffles.  The
-// cos / sin table of a block's tokens is formed once in shared memory and serves all heads.
+// Both kernels move bytes (16-byte loads and stores; a row's sums are shuffles among the lanes that hold it), and both
+// were bound by their instructions first: no division and no 64-bit product is left in the loop over rows.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -22,47 +22,49 @@ namespace {
 __device__ int g_append_check;  // set when a slot was outside [-1, n_slots) (the row was skipped)
 
 constexpr int NR_THREADS = 256;
-constexpr int NR_TABLE = 8192;  // most rotary dims x tokens of one block's table (32 KB)
 
 __device__ __forceinline__ float2 rope_cs(int64_t pos, double f, float mul) {
-  const double a = static_cast<double>(pos) * f;
-  const double n = rint(a * 0.15915494309189535);  // a / (2 pi)
-  // 2 pi as a sum of two doubles
-  const double r = fma(-n, 2.4492935982947064e-16, fma(-n, 6.2831853071795862, a));
+  const double t = static_cast<double>(pos) * f * 0.15915494309189535;  // turns
   float s, c;
-  sincosf(static_cast<float>(r), &s, &c);
+  sincospif(2.f * static_cast<float>(t - rint(t)), &s, &c);
   return make_float2(c * mul, s * mul);
 }
 
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
   #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    f[2 * i] = lo_f(u[i]);
+    f[2 * i + 1] = hi_f(u[i]);
   }
 }
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint32_t u[4];
-  #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
-// e4m3 codes of f / scale (the quotient itself, not a product with a reciprocal: a code is the nearest to it)
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale) {
-  uint32_t u[2];
-  #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] / scale, f[4 * i + 1] / scale), __NV_SATFINITE,
-                                                 __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] / scale, f[4 * i + 3] / scale),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    u[i] = lo | (hi << 16);
-  }
-  return make_uint2(u[0], u[1]);
+// The row's scale and its reciprocal.  Codes are formed from value * reciprocal: a quotient takes ten instructions an
+// element (70 -> 33 us for 4099 x 64 rows of 128), and the product, off by two roundings of 32 bits, can only choose
+// another code for a value within 2^-22 of the border of two, where the norm's own rounding chooses as much.
+__device__ __forceinline__ float2 row_scale(float amax) {
+  const float s = amax > 0.f ? amax / 448.f : 1.f;
+  return make_float2(s, 1.f / s);
+}
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
+  return make_uint2(codes2(f[0] * inv, f[1] * inv) | (codes2(f[2] * inv, f[3] * inv) << 16),
+                    codes2(f[4] * inv, f[5] * inv) | (codes2(f[6] * inv, f[7] * inv) << 16));
+}
+// s / d, off by less than a rounding: the mean of a constant row is that constant (s = c d is exact for a bf16 c)
+__device__ __forceinline__ float mean_of(float s, float d, float inv_d) {
+  const float q = s * inv_d;
+  return fmaf(fmaf(-q, d, s), inv_d, q);
 }
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
@@ -88,169 +90,195 @@ struct NormRopeArgs {
   const float* weight;
   const float* bias;
   int64_t T;
-  int H, D, norm, off, R, half;
+  int H, D, off, R, half;
   float eps, mul;
-  int NT, HB;      // tokens and heads of a block
+  int spt_log, HB;   // a block: 2^spt_log row slots a token, HB heads, (slots / 2^spt_log) tokens
   int only_rotary;  // y is x and there is no norm: the other dims stay as they are
 };
 
-// A group of G lanes holds one head row, ITER 16-byte chunks a lane (chunk = lane + G * iter).  A block covers NT
-// tokens x HB heads; the next row's loads are in flight while a row is computed.
-template <int G, int ITER, bool FP8>
+// A group of G lanes holds a head row, ITER 16-byte chunks a lane.  The rotary chunks come first: lane p holds chunk p
+// and its partner R / 16 chunks on, the two halves of eight (i, i + R/2) pairs, in two neighbouring iterations, so that
+// neither layout moves a value between lanes; the other chunks fill the rest.  A block's row slots stand for the same
+// few tokens throughout (pointers advance by whole heads) and share one table of cos and sin; RPT rows are in flight for
+// each slot before the table is formed.
+template <int G, int ITER, int NORM, bool FP8>
 __global__ void __launch_bounds__(NR_THREADS) k_norm_rope(const NormRopeArgs a) {
-  extern __shared__ float2 cs[];  // [NT][R / 2] cos, sin
+  extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
-  constexpr int SLOTS = NR_THREADS / G;
-  const int slot = threadIdx.x / G, gl = threadIdx.x % G, lane = threadIdx.x & 31;
-  const int hsplit = (a.H + a.HB - 1) / a.HB;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x / hsplit) * a.NT;
-  const int h0 = static_cast<int>(blockIdx.x % hsplit) * a.HB;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(a.NT), a.T - t0)), nh = min(a.HB, a.H - h0);
-  const int rows = nt * nh, chunks = a.D >> 3;
-  const int c_lo = a.off >> 3, half_r = a.R >> 1, c_n = a.R >> 3;  // rotary chunks [c_lo, c_lo + c_n)
+  constexpr int RPT = ITER <= 2 ? 2 : 1;
+  const int slot = threadIdx.x / G, gl = threadIdx.x % G;
+  const int spt = 1 << a.spt_log, NT = (NR_THREADS / G) >> a.spt_log;
+  const int tk = slot >> a.spt_log, hs = slot & (spt - 1);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * NT, t = t0 + tk;
+  const int half_r = a.R >> 1;
+  const int h_first = static_cast<int>(blockIdx.y) * a.HB + hs;
+  const int h_end = t < a.T ? min(a.H, static_cast<int>(blockIdx.y + 1) * a.HB) : 0;
 
-  bool mine[ITER];
-  #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    const int c = gl + G * i;
-    mine[i] = c < chunks && (!a.only_rotary || (c >= c_lo && c < c_lo + c_n));
-  }
-  auto load = [&](int row, uint4 (&v)[ITER]) {
-    const int t = row / nh, h = row - t * nh;
-    const uint16_t* p = a.x + (t0 + t) * a.ldt + (h0 + h) * a.ldh;
+  // the lane's chunks
+  int off[ITER];  // element offset, or -1
+  bool rot[(ITER + 1) / 2];
+  {
+    const int P = a.R >> 4, c_lo = a.off >> 3, n_rest = a.only_rotary ? 0 : (a.D >> 3) - 2 * P;
+    int base = 0;
     #pragma unroll
-    for (int i = 0; i < ITER; ++i)
-      v[i] = (row < rows && mine[i]) ? *reinterpret_cast<const uint4*>(p + 8 * (gl + G * i)) : make_uint4(0, 0, 0, 0);
-  };
-  uint4 nxt[ITER];
-  load(slot, nxt);
-  float w[ITER][8], b[ITER][8];
-  #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    const int c = gl + G * i;
-    #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[i][j] = a.weight && c < chunks ? a.weight[8 * c + j] : 1.f;
-      b[i][j] = a.bias && c < chunks ? a.bias[8 * c + j] : 0.f;
+    for (int i = 0; i < ITER; ++i) {
+      const int pj = i + (1 - i % 2) < ITER ? min(max(P - G * (i / 2), 0), G) : 0;  // a last odd iteration holds no pair
+      if (i % 2 == 0) rot[i / 2] = gl < pj;
+      int c = c_lo + (i % 2) * P + G * (i / 2) + gl;
+      if (gl >= pj) {
+        const int e = base + gl - pj;
+        c = e >= n_rest ? -1 : e < c_lo || P == 0 ? e : e + 2 * P;
+      }
+      base += G - pj;
+      off[i] = c < 0 ? -1 : 8 * c;
     }
   }
-  if (a.freqs) {
+  const uint16_t* px = a.x + t * a.ldt + h_first * a.ldh;
+  const int64_t xstep = spt * a.ldh;
+  uint4 v[RPT][ITER];
+  auto load = [&](int h) {
+    #pragma unroll
+    for (int k = 0; k < RPT; ++k) {
+      #pragma unroll
+      for (int i = 0; i < ITER; ++i)
+        v[k][i] = h + k * spt < h_end && off[i] >= 0 ? *reinterpret_cast<const uint4*>(px + off[i]) : make_uint4(0, 0, 0, 0);
+      px += xstep;
+    }
+  };
+  load(h_first);
+  float w[ITER][8], b[NORM == LSA_NORM_LAYER ? ITER : 1][8];
+  if (NORM != LSA_NORM_NONE) {
+    #pragma unroll
+    for (int i = 0; i < ITER; ++i)
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[i][j] = a.weight && off[i] >= 0 ? a.weight[off[i] + j] : 1.f;
+        if (NORM == LSA_NORM_LAYER) b[i][j] = a.bias && off[i] >= 0 ? a.bias[off[i] + j] : 0.f;
+      }
+  }
+  if (half_r) {
+    const int nt = static_cast<int>(min(static_cast<int64_t>(NT), a.T - t0));
     for (int i = threadIdx.x; i < nt * half_r; i += NR_THREADS) {
-      const int t = i / half_r;
-      cs[i] = rope_cs(a.pos[t0 + t], a.freqs[i - t * half_r], a.mul);
+      const int q = i / half_r;
+      cs[i] = rope_cs(a.pos[t0 + q], a.freqs[i - q * half_r], a.mul);
     }
     __syncthreads();
   }
-  for (int base = 0; base < rows; base += SLOTS) {  // uniform over the block: the shuffles need every lane
-    const int row = base + slot;
-    float f[ITER][8];
+  const float4* tab = reinterpret_cast<const float4*>(cs + tk * half_r);  // two pairs an entry
+  const float d = static_cast<float>(a.D), inv_d = 1.f / d;
+  int64_t yo = t * a.yldt + h_first * a.yldh;
+  const int64_t ystep = spt * a.yldh;
+  for (int hb = 0; hb < a.HB; hb += RPT * spt) {  // uniform over the block: the shuffles need every lane
+    const int h = h_first + hb, rows = hb + spt < a.HB ? RPT : 1;
+    if (hb) load(h);
+    float f[RPT][ITER][8];
     #pragma unroll
-    for (int i = 0; i < ITER; ++i) unpack8(nxt[i], f[i]);
-    if (base + SLOTS < rows) load(row + SLOTS, nxt);
-    const float d = static_cast<float>(a.D);
-    if (a.norm == LSA_NORM_LAYER) {
-      float s = 0.f;
+    for (int k = 0; k < RPT; ++k)
       #pragma unroll
-      for (int i = 0; i < ITER; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) s += f[i][j];
-      const float mean = group_sum<G>(s) / d;  // a division: the mean of a constant row is exact
-      #pragma unroll
-      for (int i = 0; i < ITER; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = mine[i] ? f[i][j] - mean : 0.f;  // chunks past D stay out of the sums
-    }
-    if (a.norm != LSA_NORM_NONE) {
-      float s = 0.f;
-      #pragma unroll
-      for (int i = 0; i < ITER; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) s += f[i][j] * f[i][j];
-      const float r = 1.f / sqrtf(group_sum<G>(s) / d + a.eps);
-      #pragma unroll
-      for (int i = 0; i < ITER; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * r * w[i][j] + b[i][j];
-    }
-    const int t = min(row, rows - 1) / nh;
-    if (a.freqs) {
-      const float2* tab = cs + t * half_r;
-      if (a.half) {
-        // pairs (i, i + R/2): the partner chunk is R/16 chunks away, in another lane (and iteration)
-        const int hc = a.R >> 4;
-        float g[ITER][8];
-        #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-          const int rel = gl + G * i - c_lo;
-          const int cp = min(max(rel < hc ? rel + hc : rel - hc, 0), c_n - 1) + c_lo;
-          const int src = (lane & ~(G - 1)) | (cp & (G - 1)), it = cp / G;
-          #pragma unroll
-          for (int k = 0; k < ITER; ++k)
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float o = __shfl_sync(0xffffffffu, f[k][j], src);
-              if (k == 0 || k == it) g[i][j] = o;
-            }
-        }
-        #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-          const int rel = gl + G * i - c_lo;
-          if (rel >= 0 && rel < c_n) {
-            const bool first = rel < hc;
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 e = tab[8 * (first ? rel : rel - hc) + j];
-              f[i][j] = f[i][j] * e.x + (first ? -g[i][j] : g[i][j]) * e.y;
-            }
-          }
-        }
-      } else {
-        #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-          const int rel = gl + G * i - c_lo;
-          if (rel >= 0 && rel < c_n) {
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 e = tab[4 * rel + j];
-              const float u = f[i][2 * j], v = f[i][2 * j + 1];
-              f[i][2 * j] = u * e.x - v * e.y;
-              f[i][2 * j + 1] = v * e.x + u * e.y;
-            }
-          }
-        }
-      }
-    }
-    const int h = min(row, rows - 1) - t * nh;
-    const int64_t o = (t0 + t) * a.yldt + (h0 + h) * a.yldh;
-    if (FP8) {
-      float m = 0.f;
-      #pragma unroll
-      for (int i = 0; i < ITER; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, mine[i] ? fabsf(f[i][j]) : 0.f);
-      m = group_max<G>(m);
-      const float sc = m > 0.f ? m / 448.f : 1.f;
-      if (row < rows) {
+      for (int i = 0; i < ITER; ++i) unpack8(v[k][i], f[k][i]);
+    #pragma unroll
+    for (int k = 0; k < RPT; ++k) {
+      if (k >= rows) break;
+      if (NORM == LSA_NORM_LAYER) {
+        float s = 0.f;
         #pragma unroll
         for (int i = 0; i < ITER; ++i)
-          if (mine[i])
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + o + 8 * (gl + G * i)) = codes8(f[i], sc);
-        if (gl == 0) a.scale[(t0 + t) * a.H + h0 + h] = sc;
+          #pragma unroll
+          for (int j = 0; j < 8; ++j) s += f[k][i][j];
+        const float mean = mean_of(group_sum<G>(s), d, inv_d);
+        #pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+          const float mi = off[i] >= 0 ? mean : 0.f;  // what is behind D stays out of the sums
+          #pragma unroll
+          for (int j = 0; j < 8; ++j) f[k][i][j] -= mi;
+        }
       }
-    } else if (row < rows) {
+      if (NORM != LSA_NORM_NONE) {
+        float s = 0.f;
+        #pragma unroll
+        for (int i = 0; i < ITER; ++i)
+          #pragma unroll
+          for (int j = 0; j < 8; ++j) s = fmaf(f[k][i][j], f[k][i][j], s);
+        const float r = rsqrtf(group_sum<G>(s) * inv_d + a.eps);
+        #pragma unroll
+        for (int i = 0; i < ITER; ++i)
+          #pragma unroll
+          for (int j = 0; j < 8; ++j)
+            f[k][i][j] = NORM == LSA_NORM_LAYER ? fmaf(f[k][i][j] * r, w[i][j], b[i][j]) : f[k][i][j] * r * w[i][j];
+      }
+    }
+    if (half_r) {
       #pragma unroll
-      for (int i = 0; i < ITER; ++i)
-        if (mine[i])
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + o + 8 * (gl + G * i)) = pack8(f[i]);
+      for (int q = 0; q < ITER / 2; ++q) {
+        if (!rot[q]) continue;
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (a.half) {
+            const float4 z = tab[4 * (G * q + gl) + e];  // pairs 2e, 2e + 1 of the chunk
+            #pragma unroll
+            for (int k = 0; k < RPT; ++k) {
+              float u = f[k][2 * q][2 * e], g = f[k][2 * q + 1][2 * e];
+              f[k][2 * q][2 * e] = u * z.x - g * z.y;
+              f[k][2 * q + 1][2 * e] = g * z.x + u * z.y;
+              u = f[k][2 * q][2 * e + 1], g = f[k][2 * q + 1][2 * e + 1];
+              f[k][2 * q][2 * e + 1] = u * z.z - g * z.w;
+              f[k][2 * q + 1][2 * e + 1] = g * z.z + u * z.w;
+            }
+          } else {
+            const int it = 2 * q + (e >> 1), j = 4 * (e & 1);
+            const float4 z = tab[2 * (G * q + gl + (e >> 1) * (a.R >> 4)) + (e & 1)];
+            #pragma unroll
+            for (int k = 0; k < RPT; ++k) {
+              float u = f[k][it][j], g = f[k][it][j + 1];
+              f[k][it][j] = u * z.x - g * z.y;
+              f[k][it][j + 1] = g * z.x + u * z.y;
+              u = f[k][it][j + 2], g = f[k][it][j + 3];
+              f[k][it][j + 2] = u * z.z - g * z.w;
+              f[k][it][j + 3] = g * z.z + u * z.w;
+            }
+          }
+        }
+      }
+    }
+    #pragma unroll
+    for (int k = 0; k < RPT; ++k) {
+      if (k >= rows) break;
+      const bool live = h + k * spt < h_end;
+      if (FP8) {
+        float m = 0.f;
+        #pragma unroll
+        for (int i = 0; i < ITER; ++i)
+          #pragma unroll
+          for (int j = 0; j < 8; ++j) m = fmaxf(m, off[i] >= 0 ? fabsf(f[k][i][j]) : 0.f);
+        const float2 sc = row_scale(group_max<G>(m));
+        if (live) {
+          #pragma unroll
+          for (int i = 0; i < ITER; ++i)
+            if (off[i] >= 0) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + yo + off[i]) = codes8(f[k][i], sc.y);
+          if (gl == 0) a.scale[t * a.H + h + k * spt] = sc.x;
+        }
+      } else if (live) {
+        #pragma unroll
+        for (int i = 0; i < ITER; ++i)
+          if (off[i] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + yo + off[i]) = pack8(f[k][i]);
+      }
+      yo += ystep;
     }
   }
 }
 
 template <int G, int ITER>
-cudaError_t go_norm_rope(const NormRopeArgs& a, bool fp8, unsigned grid, size_t smem, cudaStream_t s) {
-  return fp8 ? launch_pdl(k_norm_rope<G, ITER, true>, dim3(grid), dim3(NR_THREADS), smem, s, 0u, a)
-             : launch_pdl(k_norm_rope<G, ITER, false>, dim3(grid), dim3(NR_THREADS), smem, s, 0u, a);
+cudaError_t go_norm_rope(const NormRopeArgs& a, int norm, bool fp8, dim3 grid, size_t smem, cudaStream_t s) {
+  const dim3 b(NR_THREADS);
+  if (norm == LSA_NORM_NONE)
+    return fp8 ? launch_pdl(k_norm_rope<G, ITER, LSA_NORM_NONE, true>, grid, b, smem, s, 0u, a)
+               : launch_pdl(k_norm_rope<G, ITER, LSA_NORM_NONE, false>, grid, b, smem, s, 0u, a);
+  if (norm == LSA_NORM_RMS)
+    return fp8 ? launch_pdl(k_norm_rope<G, ITER, LSA_NORM_RMS, true>, grid, b, smem, s, 0u, a)
+               : launch_pdl(k_norm_rope<G, ITER, LSA_NORM_RMS, false>, grid, b, smem, s, 0u, a);
+  return fp8 ? launch_pdl(k_norm_rope<G, ITER, LSA_NORM_LAYER, true>, grid, b, smem, s, 0u, a)
+             : launch_pdl(k_norm_rope<G, ITER, LSA_NORM_LAYER, false>, grid, b, smem, s, 0u, a);
 }
 
 struct AppendArgs {
@@ -272,140 +300,147 @@ struct AppendArgs {
   float a_eps, k_eps, mul;
 };
 
-// One warp a latent row (chunks lane, lane + 32 are the 512 normed dims, chunk 64 + lane of the first 8 lanes the
-// rotary ones), another warp its index key.  Lane i forms cos and sin of pair i; the lanes that rotate fetch theirs by
-// shuffles, so there is no shared memory and no barrier on the way.
+// two bf16 of a row: neighbours, or `far` elements apart
+__device__ __forceinline__ float2 load_pair(const uint16_t* p, int far) {
+  if (far == 1) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(lo_f(u), hi_f(u));
+  }
+  return make_float2(bf16_bits_to_f32(p[0]), bf16_bits_to_f32(p[far]));
+}
+__device__ __forceinline__ void store_pair(uint16_t* p, int far, float2 v) {
+  const uint32_t u = pack2(v.x, v.y);
+  if (far == 1) {
+    *reinterpret_cast<uint32_t*>(p) = u;
+  } else {
+    p[0] = static_cast<uint16_t>(u);
+    p[far] = static_cast<uint16_t>(u >> 16);
+  }
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int far, float2 v) {
+  const uint32_t u = codes2(v.x, v.y);
+  if (far == 1) {
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(u);
+  } else {
+    p[0] = static_cast<uint8_t>(u);
+    p[far] = static_cast<uint8_t>(u >> 8);
+  }
+}
+
+// A warp a token: lane i holds 16 of the row's 512 normed dims and pair i of its rotary ones, and pair i and up to four
+// other dims of the index key, so one cos and sin a lane turns both and no value moves between lanes but the sums.  A
+// step's few rows are bound by latency, a prompt's by the latency of a row over the warps that an SM holds.
 template <bool KEYS, bool FP8>
 __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = KEYS ? static_cast<int64_t>(blockIdx.x) * 2 + (warp >> 1) : static_cast<int64_t>(blockIdx.x) * 4 + warp;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (t >= a.T) return;
-  const bool is_key = KEYS && (warp & 1);
   const int64_t slot = a.slot[t];
-  const int64_t pos = a.freqs ? a.pos[t] : 0;
-  const double fr = a.freqs ? a.freqs[lane] : 0.0;
-  if (!is_key) {
-    const uint16_t* p = a.a + t * a.lda;
-    uint4 v[3];
-    v[0] = *reinterpret_cast<const uint4*>(p + 8 * lane);
-    v[1] = *reinterpret_cast<const uint4*>(p + 8 * (lane + 32));
-    v[2] = lane < 8 ? *reinterpret_cast<const uint4*>(p + 8 * (lane + 64)) : make_uint4(0, 0, 0, 0);
-    float f[3][8];
+  const uint16_t* p = a.a + t * a.lda;
+  const uint4 v0 = *reinterpret_cast<const uint4*>(p + 8 * lane), v1 = *reinterpret_cast<const uint4*>(p + 8 * (lane + 32));
+  const int r_at = 512 + (a.half ? lane : 2 * lane), r_far = a.half ? 32 : 1;
+  float2 r = load_pair(p + r_at, r_far);
+  // the index key: its rotary pair, and dims 2 lane, 2 lane + 1 and 64 further of the others
+  const bool turn = KEYS && a.k_off >= 0;
+  const int others = KEYS ? a.d_I - (turn ? 64 : 0) : 0;
+  const int k_at = turn ? a.k_off + (a.k_half ? lane : 2 * lane) : 0, k_far = a.k_half ? 32 : 1;
+  int o_at[2];
+  float2 kr = make_float2(0.f, 0.f), ko[2] = {kr, kr};
+  if (KEYS) {
+    const uint16_t* kp = a.k + t * a.ldk;
+    if (turn) kr = load_pair(kp + k_at, k_far);
     #pragma unroll
-    for (int i = 0; i < 3; ++i) unpack8(v[i], f[i]);
-    if (a.a_weight) {
-      float w[2][8];
-      #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) w[i][j] = a.a_weight[8 * (lane + 32 * i) + j];
-      float s = 0.f;
-      #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) s += f[i][j] * f[i][j];
-      const float r = 1.f / sqrtf(warp_sum(s) * (1.f / 512.f) + a.a_eps);
-      #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * r * w[i][j];
+    for (int j = 0; j < 2; ++j) {
+      const int e = 2 * lane + 64 * j;
+      o_at[j] = e >= others ? -1 : turn && e >= a.k_off ? e + 64 : e;
+      if (o_at[j] >= 0) ko[j] = load_pair(kp + o_at[j], 1);
     }
-    if (a.freqs) {
-      const float2 e = rope_cs(pos, fr, a.mul);
-      if (a.half) {
+  }
+  float2 cs = make_float2(1.f, 0.f);
+  if (a.freqs) cs = rope_cs(a.pos[t], a.freqs[lane], a.mul);
+  float f[2][8];
+  unpack8(v0, f[0]);
+  unpack8(v1, f[1]);
+  const bool write = slot >= 0 && slot < a.n_slots;
+  if (!write && slot != -1 && lane == 0) atomicExch(&g_append_check, 1);
+  if (a.a_weight) {
+    float s = 0.f;
+    #pragma unroll
+    for (int i = 0; i < 2; ++i)
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) s = fmaf(f[i][j], f[i][j], s);
+    const float q = rsqrtf(warp_sum(s) * (1.f / 512.f) + a.a_eps);
+    const bool wide = (reinterpret_cast<uintptr_t>(a.a_weight) & 15) == 0;
+    #pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* w = a.a_weight + 8 * (lane + 32 * i);
+      if (wide) {
+        const float4 x = reinterpret_cast<const float4*>(w)[0], y = reinterpret_cast<const float4*>(w)[1];
+        const float g[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float g = __shfl_xor_sync(0xffffffffu, f[2][j], 4);
-          const int pair = 8 * (lane & 3) + j;
-          const float c = __shfl_sync(0xffffffffu, e.x, pair), s = __shfl_sync(0xffffffffu, e.y, pair);
-          f[2][j] = f[2][j] * c + ((lane & 4) ? g : -g) * s;
-        }
+        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * q * g[j];
       } else {
         #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int pair = (4 * lane + j) & 31;
-          const float c = __shfl_sync(0xffffffffu, e.x, pair), s = __shfl_sync(0xffffffffu, e.y, pair);
-          const float u = f[2][2 * j], w = f[2][2 * j + 1];
-          f[2][2 * j] = u * c - w * s;
-          f[2][2 * j + 1] = w * c + u * s;
-        }
+        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * q * w[j];
       }
     }
-    if (slot < 0 || slot >= a.n_slots) {
-      if (slot != -1 && lane == 0) atomicExch(&g_append_check, 1);
-      return;
-    }
+  }
+  if (a.freqs) r = make_float2(r.x * cs.x - r.y * cs.y, r.y * cs.x + r.x * cs.y);
+  if (write) {
     uint16_t* o = a.kv + slot * 576;
     *reinterpret_cast<uint4*>(o + 8 * lane) = pack8(f[0]);
     *reinterpret_cast<uint4*>(o + 8 * (lane + 32)) = pack8(f[1]);
-    if (lane < 8) *reinterpret_cast<uint4*>(o + 8 * (lane + 64)) = pack8(f[2]);
-  } else {
-    const int chunks = a.d_I >> 3;
-    const bool mine = lane < chunks;
-    float f[8];
-    unpack8(mine ? *reinterpret_cast<const uint4*>(a.k + t * a.ldk + 8 * lane) : make_uint4(0, 0, 0, 0), f);
-    const float d = static_cast<float>(a.d_I);
-    if (a.k_norm == LSA_NORM_LAYER) {
-      float s = 0.f;
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) s += f[j];
-      const float mean = warp_sum(s) / d;
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = mine ? f[j] - mean : 0.f;
+    store_pair(o + r_at, r_far, r);
+  }
+  if (!KEYS) return;
+  const float d = static_cast<float>(a.d_I), inv_d = 1.f / d;
+  if (a.k_norm == LSA_NORM_LAYER) {
+    const float mean = mean_of(warp_sum(kr.x + kr.y + ((ko[0].x + ko[0].y) + (ko[1].x + ko[1].y))), d, inv_d);
+    if (turn) {
+      kr.x -= mean;
+      kr.y -= mean;
     }
-    if (a.k_norm != LSA_NORM_NONE) {
-      float s = 0.f;
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) s += f[j] * f[j];
-      const float r = 1.f / sqrtf(warp_sum(s) / d + a.k_eps);
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = a.k_weight && mine ? a.k_weight[8 * lane + j] : 1.f;
-        const float b = a.k_bias && mine ? a.k_bias[8 * lane + j] : 0.f;
-        f[j] = f[j] * r * w + b;
+    #pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (o_at[j] >= 0) {
+        ko[j].x -= mean;
+        ko[j].y -= mean;
       }
-    }
-    if (a.freqs && a.k_off >= 0) {
-      const float2 e = rope_cs(pos, fr, a.mul);
-      const int rel = lane - (a.k_off >> 3);
-      const bool rot = rel >= 0 && rel < 8;
-      if (a.k_half) {
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float g = __shfl_sync(0xffffffffu, f[j], (rel < 4 ? lane + 4 : lane - 4) & 31);
-          const int pair = 8 * (rel & 3) + j;
-          const float c = __shfl_sync(0xffffffffu, e.x, pair), s = __shfl_sync(0xffffffffu, e.y, pair);
-          if (rot) f[j] = f[j] * c + (rel < 4 ? -g : g) * s;
-        }
-      } else {
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int pair = (4 * rel + j) & 31;
-          const float c = __shfl_sync(0xffffffffu, e.x, pair), s = __shfl_sync(0xffffffffu, e.y, pair);
-          const float u = f[2 * j], w = f[2 * j + 1];
-          if (rot) {
-            f[2 * j] = u * c - w * s;
-            f[2 * j + 1] = w * c + u * s;
-          }
-        }
-      }
-    }
-    if (FP8) {
-      float m = 0.f;
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, mine ? fabsf(f[j]) : 0.f);
-      m = warp_max(m);
-      const float sc = m > 0.f ? m / 448.f : 1.f;
-      if (slot < 0 || slot >= a.n_slots) return;
-      if (mine)
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.kc) + slot * a.d_I + 8 * lane) = codes8(f, sc);
-      if (lane == 0) a.k_scale[slot] = sc;
-    } else {
-      if (slot < 0 || slot >= a.n_slots) return;
-      if (mine) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.kc) + slot * a.d_I + 8 * lane) = pack8(f);
-    }
+  }
+  if (a.k_norm != LSA_NORM_NONE) {
+    const float s = fmaf(kr.x, kr.x, kr.y * kr.y) +
+                    (fmaf(ko[0].x, ko[0].x, ko[0].y * ko[0].y) + fmaf(ko[1].x, ko[1].x, ko[1].y * ko[1].y));
+    const float q = rsqrtf(warp_sum(s) * inv_d + a.k_eps);
+    auto apply = [&](float2& v, int at, int far) {
+      const float w0 = a.k_weight ? a.k_weight[at] : 1.f, w1 = a.k_weight ? a.k_weight[at + far] : 1.f;
+      const float b0 = a.k_bias ? a.k_bias[at] : 0.f, b1 = a.k_bias ? a.k_bias[at + far] : 0.f;
+      v = make_float2(fmaf(v.x * q, w0, b0), fmaf(v.y * q, w1, b1));
+    };
+    if (turn) apply(kr, k_at, k_far);
+    #pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (o_at[j] >= 0) apply(ko[j], o_at[j], 1);
+  }
+  if (turn) kr = make_float2(kr.x * cs.x - kr.y * cs.y, kr.y * cs.x + kr.x * cs.y);
+  if (FP8) {
+    const float m = fmaxf(fmaxf(fabsf(kr.x), fabsf(kr.y)),
+                          fmaxf(fmaxf(fabsf(ko[0].x), fabsf(ko[0].y)), fmaxf(fabsf(ko[1].x), fabsf(ko[1].y))));
+    const float2 sc = row_scale(warp_max(m));
+    if (!write) return;
+    uint8_t* o = static_cast<uint8_t*>(a.kc) + slot * a.d_I;
+    if (turn) store_codes(o + k_at, k_far, make_float2(kr.x * sc.y, kr.y * sc.y));
+    #pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (o_at[j] >= 0) store_codes(o + o_at[j], 1, make_float2(ko[j].x * sc.y, ko[j].y * sc.y));
+    if (lane == 0) a.k_scale[slot] = sc.x;
+  } else if (write) {
+    uint16_t* o = static_cast<uint16_t*>(a.kc) + slot * a.d_I;
+    if (turn) store_pair(o + k_at, k_far, kr);
+    #pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (o_at[j] >= 0) store_pair(o + o_at[j], 1, ko[j]);
   }
 }
 
@@ -432,7 +467,6 @@ int launch_norm_rope(const void* x, int64_t ldt, int64_t ldh, int64_t T, int H, 
   a.T = T;
   a.H = H;
   a.D = D;
-  a.norm = norm;
   a.off = off;
   a.R = freqs ? R : 0;
   a.half = layout == LSA_ROPE_HALF;
@@ -440,45 +474,45 @@ int launch_norm_rope(const void* x, int64_t ldt, int64_t ldh, int64_t T, int H, 
   a.mul = mul;
   const bool fp8 = dtype == LSA_FP8_E4M3;
   a.only_rotary = !fp8 && norm == LSA_NORM_NONE && x == y && ldt == yldt && ldh == yldh;
-  // lanes a row: its 16-byte chunks spread over a power of two of lanes, with one or three chunks a lane where that
-  // leaves none idle, else a whole warp
+  // lanes a row: two 16-byte chunks a lane (a rotary pair of chunks lies in one lane), three where that leaves none idle
   const int n = D >> 3;
-  int G = 32, it = (n + 31) / 32;
-  for (int g = 4; g <= 16; g *= 2)
-    if (n == g || n == 3 * g) {
+  int G = 32, it = n <= 64 ? 2 : n <= 96 && a.R / 16 <= 32 ? 3 : 4;
+  for (int g = 16; g >= 2; g /= 2) {
+    if (n <= 2 * g) {
       G = g;
-      it = n / g;
+      it = 2;
+    } else if (n == 3 * g && g >= 4 && a.R / 16 <= g) {
+      G = g;
+      it = 3;
+      break;
     }
-  if (n < 4) {
-    G = 4;
-    it = 1;
   }
-  // a block's rows: four to a group of lanes when there are many rows (more loads in flight for each pass through the
-  // table), one when the whole call would not fill the GPU's 8 blocks an SM
+  // a block's row slots go to one token as far as it has heads; two passes over its heads where the blocks are many
   const int slots = NR_THREADS / G;
-  const int64_t total = T * H;
-  const int64_t want = total > static_cast<int64_t>(sm_count()) * 8 * slots * 2 ? 4 * slots : slots;
-  if (H >= want) {
-    a.NT = 1;
-    a.HB = static_cast<int>(want);
-  } else {
-    a.HB = H;
-    a.NT = static_cast<int>(want / H);
-    if (a.R > 0 && a.NT > NR_TABLE / a.R) a.NT = NR_TABLE / a.R;
-    if (a.NT < 1) a.NT = 1;
-  }
-  const int64_t grid = cdiv(T, a.NT) * cdiv(H, a.HB);
-  if (grid > 0x7FFFFFFF) return LSA_ERR_UNSUPPORTED;
-  const size_t smem = static_cast<size_t>(a.NT) * (a.R / 2) * sizeof(float2);
-  const unsigned g = static_cast<unsigned>(grid);
+  a.spt_log = 0;
+  while ((1 << a.spt_log) < slots && (1 << a.spt_log) < H) ++a.spt_log;
+  const int spt = 1 << a.spt_log, NT = slots >> a.spt_log;
+  a.HB = spt;
+  while (a.HB < H && a.HB < 4 * spt && cdiv(T, NT) * cdiv(H, 2 * a.HB) >= 4 * sm_count()) a.HB *= 2;
+  const int64_t gx = cdiv(T, NT);
+  if (gx > 0x7FFFFFFF) return LSA_ERR_UNSUPPORTED;
+  const size_t smem = static_cast<size_t>(NT) * (a.R / 2) * sizeof(float2);
+  const dim3 g(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(H, a.HB)));
   cudaError_t e = cudaErrorInvalidValue;
-  if (G == 4) e = it == 1 ? go_norm_rope<4, 1>(a, fp8, g, smem, s) : go_norm_rope<4, 3>(a, fp8, g, smem, s);
-  else if (G == 8) e = it == 1 ? go_norm_rope<8, 1>(a, fp8, g, smem, s) : go_norm_rope<8, 3>(a, fp8, g, smem, s);
-  else if (G == 16) e = it == 1 ? go_norm_rope<16, 1>(a, fp8, g, smem, s) : go_norm_rope<16, 3>(a, fp8, g, smem, s);
-  else if (it == 1) e = go_norm_rope<32, 1>(a, fp8, g, smem, s);
-  else if (it == 2) e = go_norm_rope<32, 2>(a, fp8, g, smem, s);
-  else if (it == 3) e = go_norm_rope<32, 3>(a, fp8, g, smem, s);
-  else if (it == 4) e = go_norm_rope<32, 4>(a, fp8, g, smem, s);
+  if (it == 2) {
+    if (G == 2) e = go_norm_rope<2, 2>(a, norm, fp8, g, smem, s);
+    else if (G == 4) e = go_norm_rope<4, 2>(a, norm, fp8, g, smem, s);
+    else if (G == 8) e = go_norm_rope<8, 2>(a, norm, fp8, g, smem, s);
+    else if (G == 16) e = go_norm_rope<16, 2>(a, norm, fp8, g, smem, s);
+    else e = go_norm_rope<32, 2>(a, norm, fp8, g, smem, s);
+  } else if (it == 3) {
+    if (G == 4) e = go_norm_rope<4, 3>(a, norm, fp8, g, smem, s);
+    else if (G == 8) e = go_norm_rope<8, 3>(a, norm, fp8, g, smem, s);
+    else if (G == 16) e = go_norm_rope<16, 3>(a, norm, fp8, g, smem, s);
+    else e = go_norm_rope<32, 3>(a, norm, fp8, g, smem, s);
+  } else {
+    e = go_norm_rope<32, 4>(a, norm, fp8, g, smem, s);
+  }
   return cuda_status(e);
 }
 
@@ -511,7 +545,7 @@ int launch_cache_append(const void* x, int64_t ldx, const float* x_weight, float
   a.a_eps = x_eps;
   a.k_eps = k_eps;
   a.mul = mul;
-  const int64_t grid = cdiv(T, k ? 2 : 4);
+  const int64_t grid = cdiv(T, 4);
   if (grid > 0x7FFFFFFF) return LSA_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid)), b(128);
   if (!k) return cuda_status(launch_pdl(k_cache_append<false, false>, g, b, 0, s, 0u, a));
