@@ -21,7 +21,7 @@ namespace {
 
 __device__ int g_append_check;  // set when a slot was outside [-1, n_slots) (the row was skipped)
 
-constexpr int NR_THREADS = 256;
+constexpr int NR_THREADS = 128;
 
 __device__ __forceinline__ float2 rope_cs(int64_t pos, double f, float mul) {
   const double t = static_cast<double>(pos) * f * 0.15915494309189535;  // turns
@@ -44,28 +44,70 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     f[2 * i + 1] = hi_f(u[i]);
   }
 }
+// eight results, rounded to bf16 (the caches' and queries' type)
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack2(f[0].x, f[0].y), pack2(f[1].x, f[1].y), pack2(f[2].x, f[2].y), pack2(f[3].x, f[3].y));
+}
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
-// The row's scale and its reciprocal.  Codes are formed from value * reciprocal: a quotient takes ten instructions an
-// element (70 -> 33 us for 4099 x 64 rows of 128), and the product, off by two roundings of 32 bits, can only choose
-// another code for a value within 2^-22 of the border of two, where the norm's own rounding chooses as much.
+// The row's scale and its reciprocal (0 where that would overflow).  Codes are formed from value * reciprocal: a quotient
+// takes ten instructions an element, and the product, off by two roundings of 32 bits, can only choose another code for a
+// value within 2^-22 of the border of two, where the norm's own rounding chooses as much.
 __device__ __forceinline__ float2 row_scale(float amax) {
-  const float s = amax > 0.f ? amax / 448.f : 1.f;
-  return make_float2(s, 1.f / s);
+  const float s = amax > 0.f ? amax * (1.f / 448.f) : 1.f;
+  return make_float2(s, s > 1e-35f ? __fdividef(1.f, s) : 0.f);
 }
-__device__ __forceinline__ uint32_t codes2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t codes2(float2 v, float inv) {
+  uint16_t u;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(u) : "f"(v.y * inv), "f"(v.x * inv));
+  return u;
 }
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
-  return make_uint2(codes2(f[0] * inv, f[1] * inv) | (codes2(f[2] * inv, f[3] * inv) << 16),
-                    codes2(f[4] * inv, f[5] * inv) | (codes2(f[6] * inv, f[7] * inv) << 16));
+// the values over the scale where there is no reciprocal: codes are then formed with 1
+template <int N>
+__device__ __forceinline__ float tiny_row(float2 (&f)[N], const float2& sc) {
+  if (sc.y != 0.f) return sc.y;
+  #pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = make_float2(f[i].x / sc.x, f[i].y / sc.x);
+  return 1.f;
+}
+__device__ __forceinline__ uint2 codes8(float2 (&f)[4], const float2& sc) {
+  const float inv = tiny_row(f, sc);
+  return make_uint2(codes2(f[0], inv) | (codes2(f[1], inv) << 16), codes2(f[2], inv) | (codes2(f[3], inv) << 16));
 }
 // s / d, off by less than a rounding: the mean of a constant row is that constant (s = c d is exact for a bf16 c)
 __device__ __forceinline__ float mean_of(float s, float d, float inv_d) {
   const float q = s * inv_d;
   return fmaf(fmaf(-q, d, s), inv_d, q);
 }
+// two 32-bit operations an instruction
+__device__ __forceinline__ uint64_t bits(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 floats(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return floats(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return floats(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return floats(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
   #pragma unroll
@@ -92,28 +134,35 @@ struct NormRopeArgs {
   int64_t T;
   int H, D, off, R, half;
   float eps, mul;
-  int spt_log, HB;   // a block: 2^spt_log row slots a token, HB heads, (slots / 2^spt_log) tokens
+  int spt_log, HB, TB;  // a block: 2^spt_log row slots a token, HB heads, TB times (slots / 2^spt_log) tokens
   int only_rotary;  // y is x and there is no norm: the other dims stay as they are
 };
 
 // A group of G lanes holds a head row, ITER 16-byte chunks a lane.  The rotary chunks come first: lane p holds chunk p
 // and its partner R / 16 chunks on, the two halves of eight (i, i + R/2) pairs, in two neighbouring iterations, so that
-// neither layout moves a value between lanes; the other chunks fill the rest.  A block's row slots stand for the same
-// few tokens throughout (pointers advance by whole heads) and share one table of cos and sin; RPT rows are in flight for
-// each slot before the table is formed.
+// neither layout moves a value between lanes; the other chunks fill the rest.  A block forms one table of cos and sin
+// for its tokens (the chain of loads, 64-bit products and sincospif takes longer than 64 rows) and walks their heads, RPT
+// rows a slot at a time, with the next rows' loads in flight; weights and table lie in shared memory, because 32 registers
+// of weights halve the warps of an SM (70 us against 45 for 8192 x 64 rows of 128 dims).  Products and sums go two an
+// instruction.  Small blocks (128 threads, six an SM) wait for each other least: 43.4 us against 44.6 at 256 threads and
+// 70 at 512; a grid of resident blocks with two tables in turn took 55.
+// 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 43.4 us, 6190 GB/s.  2047 x 128 rows of 64, no norm: 10.9 us,
+// 6170 GB/s.  4099 x 64 rows of 128, layer norm, to codes: 29.4 us, 3460 GB/s, bound by its instructions (three reductions
+// and a scale a row, 17 operations an element).
 template <int G, int ITER, int NORM, bool FP8>
-__global__ void __launch_bounds__(NR_THREADS) k_norm_rope(const NormRopeArgs a) {
-  extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin
+__global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(const NormRopeArgs a) {
+  extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin | weight [D] | bias [D]
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   constexpr int RPT = ITER <= 2 ? 2 : 1;
   const int slot = threadIdx.x / G, gl = threadIdx.x % G;
   const int spt = 1 << a.spt_log, NT = (NR_THREADS / G) >> a.spt_log;
   const int tk = slot >> a.spt_log, hs = slot & (spt - 1);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * NT, t = t0 + tk;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * NT * a.TB;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(NT) * a.TB, a.T - t0));  // tokens of this block
   const int half_r = a.R >> 1;
   const int h_first = static_cast<int>(blockIdx.y) * a.HB + hs;
-  const int h_end = t < a.T ? min(a.H, static_cast<int>(blockIdx.y + 1) * a.HB) : 0;
+  const int h_end = min(a.H, static_cast<int>(blockIdx.y + 1) * a.HB);
 
   // the lane's chunks
   int off[ITER];  // element offset, or -1
@@ -134,136 +183,186 @@ __global__ void __launch_bounds__(NR_THREADS) k_norm_rope(const NormRopeArgs a) 
       off[i] = c < 0 ? -1 : 8 * c;
     }
   }
-  const uint16_t* px = a.x + t * a.ldt + h_first * a.ldh;
-  const int64_t xstep = spt * a.ldh;
+  // rows k of the slot's next step: token tl, heads h_first + lh + k spt
   uint4 v[RPT][ITER];
-  auto load = [&](int h) {
+  int tl = tk, lh = 0;
+  auto load = [&]() {
+    const uint16_t* px = a.x + (t0 + tl) * a.ldt + (h_first + lh) * a.ldh;
     #pragma unroll
     for (int k = 0; k < RPT; ++k) {
+      const bool live = tl < nt && h_first + lh + k * spt < h_end;
       #pragma unroll
       for (int i = 0; i < ITER; ++i)
-        v[k][i] = h + k * spt < h_end && off[i] >= 0 ? *reinterpret_cast<const uint4*>(px + off[i]) : make_uint4(0, 0, 0, 0);
-      px += xstep;
+        v[k][i] = live && off[i] >= 0 ? *reinterpret_cast<const uint4*>(px + k * spt * a.ldh + off[i]) : make_uint4(0, 0, 0, 0);
+    }
+    lh += RPT * spt;
+    if (lh >= a.HB) {
+      lh = 0;
+      tl += NT;
     }
   };
-  load(h_first);
-  float w[ITER][8], b[NORM == LSA_NORM_LAYER ? ITER : 1][8];
-  if (NORM != LSA_NORM_NONE) {
-    #pragma unroll
-    for (int i = 0; i < ITER; ++i)
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        w[i][j] = a.weight && off[i] >= 0 ? a.weight[off[i] + j] : 1.f;
-        if (NORM == LSA_NORM_LAYER) b[i][j] = a.bias && off[i] >= 0 ? a.bias[off[i] + j] : 0.f;
+  load();
+  // Entries of four floats (two pairs; four weights) that the lanes of a row read together lie side by side.
+  float* w_s = reinterpret_cast<float*>(cs + static_cast<size_t>(NT) * a.TB * half_r);
+  float* b_s = w_s + a.D;
+  const int P = a.R >> 4;
+  float* cf = reinterpret_cast<float*>(cs);
+  auto put = [&](int q, int p, float2 v) {  // token q, pair p: an entry is cos of two pairs, then sin
+    const int e = a.half ? ((p & 7) >> 1) * P + (p >> 3) : ((p & 3) >> 1) * 2 * P + (p >> 2);
+    float* o = cf + 2 * q * half_r + 4 * e + (p & 1);
+    o[0] = v.x;
+    o[2] = v.y;
+  };
+  auto weight_at = [&](int i) { return 4 * (((i & 7) >> 2) * (a.D >> 3) + (i >> 3)) + (i & 3); };
+  {
+    // the first of each thread's loads go out together
+    const int i0 = threadIdx.x, q0 = half_r ? i0 / half_r : 0;
+    const bool any = i0 < nt * half_r, wany = NORM != LSA_NORM_NONE && i0 < a.D;
+    const int64_t pos = any ? a.pos[t0 + q0] : 0;
+    const double fr = any ? a.freqs[i0 - q0 * half_r] : 0.0;
+    const float w0 = wany && a.weight ? a.weight[i0] : 1.f, b0 = wany && a.bias ? a.bias[i0] : 0.f;
+    if (any) put(q0, i0 - q0 * half_r, rope_cs(pos, fr, a.mul));
+    if (wany) {
+      w_s[weight_at(i0)] = w0;
+      if (NORM == LSA_NORM_LAYER) b_s[weight_at(i0)] = b0;
+    }
+    for (int i = i0 + NR_THREADS; i < nt * half_r; i += NR_THREADS) {
+      const int q = i / half_r;
+      put(q, i - q * half_r, rope_cs(a.pos[t0 + q], a.freqs[i - q * half_r], a.mul));
+    }
+    if (NORM != LSA_NORM_NONE)
+      for (int i = i0 + NR_THREADS; i < a.D; i += NR_THREADS) {
+        w_s[weight_at(i)] = a.weight ? a.weight[i] : 1.f;
+        if (NORM == LSA_NORM_LAYER) b_s[weight_at(i)] = a.bias ? a.bias[i] : 0.f;
       }
   }
-  if (half_r) {
-    const int nt = static_cast<int>(min(static_cast<int64_t>(NT), a.T - t0));
-    for (int i = threadIdx.x; i < nt * half_r; i += NR_THREADS) {
-      const int q = i / half_r;
-      cs[i] = rope_cs(a.pos[t0 + q], a.freqs[i - q * half_r], a.mul);
-    }
-    __syncthreads();
-  }
-  const float4* tab = reinterpret_cast<const float4*>(cs + tk * half_r);  // two pairs an entry
+  __syncthreads();
   const float d = static_cast<float>(a.D), inv_d = 1.f / d;
-  int64_t yo = t * a.yldt + h_first * a.yldh;
-  const int64_t ystep = spt * a.yldh;
-  for (int hb = 0; hb < a.HB; hb += RPT * spt) {  // uniform over the block: the shuffles need every lane
-    const int h = h_first + hb, rows = hb + spt < a.HB ? RPT : 1;
-    if (hb) load(h);
-    float f[RPT][ITER][8];
-    #pragma unroll
-    for (int k = 0; k < RPT; ++k)
+  for (int tb = 0; tb < a.TB && NT * tb < nt; ++tb) {  // uniform over the block: the shuffles need every lane
+    const int tq = NT * tb + tk;
+    const int64_t t = t0 + tq;
+    const float4* tab = reinterpret_cast<const float4*>(cs + min(tq, nt - 1) * half_r);  // two pairs an entry
+    for (int hb = 0; hb < a.HB; hb += RPT * spt) {
+      const int h = h_first + hb, rows = hb + spt < a.HB ? RPT : 1;
+      float2 f[RPT][ITER][4];
       #pragma unroll
-      for (int i = 0; i < ITER; ++i) unpack8(v[k][i], f[k][i]);
-    #pragma unroll
-    for (int k = 0; k < RPT; ++k) {
-      if (k >= rows) break;
-      if (NORM == LSA_NORM_LAYER) {
-        float s = 0.f;
-        #pragma unroll
-        for (int i = 0; i < ITER; ++i)
-          #pragma unroll
-          for (int j = 0; j < 8; ++j) s += f[k][i][j];
-        const float mean = mean_of(group_sum<G>(s), d, inv_d);
+      for (int k = 0; k < RPT; ++k)
         #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-          const float mi = off[i] >= 0 ? mean : 0.f;  // what is behind D stays out of the sums
+          const uint32_t u[4] = {v[k][i].x, v[k][i].y, v[k][i].z, v[k][i].w};
           #pragma unroll
-          for (int j = 0; j < 8; ++j) f[k][i][j] -= mi;
+          for (int j = 0; j < 4; ++j) f[k][i][j] = make_float2(lo_f(u[j]), hi_f(u[j]));
         }
-      }
+      load();
       if (NORM != LSA_NORM_NONE) {
-        float s = 0.f;
+        float r[RPT];
         #pragma unroll
-        for (int i = 0; i < ITER; ++i)
-          #pragma unroll
-          for (int j = 0; j < 8; ++j) s = fmaf(f[k][i][j], f[k][i][j], s);
-        const float r = rsqrtf(group_sum<G>(s) * inv_d + a.eps);
-        #pragma unroll
-        for (int i = 0; i < ITER; ++i)
-          #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            f[k][i][j] = NORM == LSA_NORM_LAYER ? fmaf(f[k][i][j] * r, w[i][j], b[i][j]) : f[k][i][j] * r * w[i][j];
-      }
-    }
-    if (half_r) {
-      #pragma unroll
-      for (int q = 0; q < ITER / 2; ++q) {
-        if (!rot[q]) continue;
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (a.half) {
-            const float4 z = tab[4 * (G * q + gl) + e];  // pairs 2e, 2e + 1 of the chunk
+        for (int k = 0; k < RPT; ++k) {
+          if (NORM == LSA_NORM_LAYER) {
+            float2 s = f[k][0][0];
             #pragma unroll
-            for (int k = 0; k < RPT; ++k) {
-              float u = f[k][2 * q][2 * e], g = f[k][2 * q + 1][2 * e];
-              f[k][2 * q][2 * e] = u * z.x - g * z.y;
-              f[k][2 * q + 1][2 * e] = g * z.x + u * z.y;
-              u = f[k][2 * q][2 * e + 1], g = f[k][2 * q + 1][2 * e + 1];
-              f[k][2 * q][2 * e + 1] = u * z.z - g * z.w;
-              f[k][2 * q + 1][2 * e + 1] = g * z.z + u * z.w;
+            for (int i = 0; i < ITER; ++i)
+              #pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (i + j > 0) s = add2(s, f[k][i][j]);
+            const float mean = mean_of(group_sum<G>(s.x + s.y), d, inv_d);
+            #pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+              const float2 mi = both(off[i] >= 0 ? -mean : 0.f);  // what is behind D stays out of the sums
+              #pragma unroll
+              for (int j = 0; j < 4; ++j) f[k][i][j] = add2(f[k][i][j], mi);
             }
-          } else {
-            const int it = 2 * q + (e >> 1), j = 4 * (e & 1);
-            const float4 z = tab[2 * (G * q + gl + (e >> 1) * (a.R >> 4)) + (e & 1)];
+          }
+          float2 s = mul2(f[k][0][0], f[k][0][0]);
+          #pragma unroll
+          for (int i = 0; i < ITER; ++i)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (i + j > 0) s = fma2(f[k][i][j], f[k][i][j], s);
+          r[k] = rsqrtf(group_sum<G>(s.x + s.y) * inv_d + a.eps);
+        }
+        #pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+          const int o = max(off[i], 0) >> 3;
+          #pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float4 w = *reinterpret_cast<const float4*>(w_s + 4 * (o + q * (a.D >> 3)));
+            const float4 b = NORM == LSA_NORM_LAYER ? *reinterpret_cast<const float4*>(b_s + 4 * (o + q * (a.D >> 3)))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
             #pragma unroll
             for (int k = 0; k < RPT; ++k) {
-              float u = f[k][it][j], g = f[k][it][j + 1];
-              f[k][it][j] = u * z.x - g * z.y;
-              f[k][it][j + 1] = g * z.x + u * z.y;
-              u = f[k][it][j + 2], g = f[k][it][j + 3];
-              f[k][it][j + 2] = u * z.z - g * z.w;
-              f[k][it][j + 3] = g * z.z + u * z.w;
+              float2* g = f[k][i] + 2 * q;
+              g[0] = mul2(g[0], both(r[k]));
+              g[1] = mul2(g[1], both(r[k]));
+              if (NORM == LSA_NORM_LAYER) {
+                g[0] = fma2(g[0], make_float2(w.x, w.y), make_float2(b.x, b.y));
+                g[1] = fma2(g[1], make_float2(w.z, w.w), make_float2(b.z, b.w));
+              } else {
+                g[0] = mul2(g[0], make_float2(w.x, w.y));
+                g[1] = mul2(g[1], make_float2(w.z, w.w));
+              }
             }
           }
         }
       }
-    }
-    #pragma unroll
-    for (int k = 0; k < RPT; ++k) {
-      if (k >= rows) break;
-      const bool live = h + k * spt < h_end;
-      if (FP8) {
-        float m = 0.f;
+      if (half_r) {
         #pragma unroll
-        for (int i = 0; i < ITER; ++i)
+        for (int q = 0; q < ITER / 2; ++q) {
+          if (!rot[q]) continue;
           #pragma unroll
-          for (int j = 0; j < 8; ++j) m = fmaxf(m, off[i] >= 0 ? fabsf(f[k][i][j]) : 0.f);
-        const float2 sc = row_scale(group_max<G>(m));
-        if (live) {
+          for (int e = 0; e < 4; ++e) {
+            if (a.half) {
+              const float4 z = tab[e * P + G * q + gl];  // cos of pairs 2e, 2e + 1 of the chunk, then sin
+              const float2 c = make_float2(z.x, z.y), n = make_float2(z.z, z.w), m = make_float2(-z.z, -z.w);
+              #pragma unroll
+              for (int k = 0; k < RPT; ++k) {
+                const float2 u = f[k][2 * q][e], g = f[k][2 * q + 1][e];
+                f[k][2 * q][e] = fma2(g, m, mul2(u, c));
+                f[k][2 * q + 1][e] = fma2(u, n, mul2(g, c));
+              }
+            } else {
+              const int it = 2 * q + (e >> 1), j = 2 * (e & 1);
+              const float4 z = tab[(e & 1) * 2 * P + G * q + gl + (e >> 1) * P];
+              #pragma unroll
+              for (int k = 0; k < RPT; ++k) {
+                float2 u = f[k][it][j];
+                f[k][it][j] = make_float2(u.x * z.x - u.y * z.z, u.y * z.x + u.x * z.z);
+                u = f[k][it][j + 1];
+                f[k][it][j + 1] = make_float2(u.x * z.y - u.y * z.w, u.y * z.y + u.x * z.w);
+              }
+            }
+          }
+        }
+      }
+      const int64_t yo = t * a.yldt + h * a.yldh;
+      #pragma unroll
+      for (int k = 0; k < RPT; ++k) {
+        if (k >= rows) break;
+        const bool live = tq < nt && h + k * spt < h_end;
+        if (FP8) {
+          float m = 0.f;
+          #pragma unroll
+          for (int i = 0; i < ITER; ++i) {
+            float mi = 0.f;
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) mi = fmaxf(mi, fmaxf(fabsf(f[k][i][j].x), fabsf(f[k][i][j].y)));
+            m = fmaxf(m, off[i] >= 0 ? mi : 0.f);
+          }
+          const float2 sc = row_scale(group_max<G>(m));
+          if (live) {
+            uint8_t* py = static_cast<uint8_t*>(a.y) + yo + k * spt * a.yldh;
+            #pragma unroll
+            for (int i = 0; i < ITER; ++i)
+              if (off[i] >= 0) *reinterpret_cast<uint2*>(py + off[i]) = codes8(f[k][i], sc);
+            if (gl == 0) a.scale[t * a.H + h + k * spt] = sc.x;
+          }
+        } else if (live) {
+          uint16_t* py = static_cast<uint16_t*>(a.y) + yo + k * spt * a.yldh;
           #pragma unroll
           for (int i = 0; i < ITER; ++i)
-            if (off[i] >= 0) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + yo + off[i]) = codes8(f[k][i], sc.y);
-          if (gl == 0) a.scale[t * a.H + h + k * spt] = sc.x;
+            if (off[i] >= 0) *reinterpret_cast<uint4*>(py + off[i]) = pack8(f[k][i]);
         }
-      } else if (live) {
-        #pragma unroll
-        for (int i = 0; i < ITER; ++i)
-          if (off[i] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + yo + off[i]) = pack8(f[k][i]);
       }
-      yo += ystep;
     }
   }
 }
@@ -317,8 +416,10 @@ __device__ __forceinline__ void store_pair(uint16_t* p, int far, float2 v) {
     p[far] = static_cast<uint16_t>(u >> 16);
   }
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int far, float2 v) {
-  const uint32_t u = codes2(v.x, v.y);
+__device__ __forceinline__ void store_codes(uint8_t* p, int far, float2 v, const float2& sc) {
+  float2 f[1] = {v};
+  const float inv = tiny_row(f, sc);
+  const uint32_t u = codes2(f[0], inv);
   if (far == 1) {
     *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(u);
   } else {
@@ -430,10 +531,10 @@ __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
     const float2 sc = row_scale(warp_max(m));
     if (!write) return;
     uint8_t* o = static_cast<uint8_t*>(a.kc) + slot * a.d_I;
-    if (turn) store_codes(o + k_at, k_far, make_float2(kr.x * sc.y, kr.y * sc.y));
+    if (turn) store_codes(o + k_at, k_far, kr, sc);
     #pragma unroll
     for (int j = 0; j < 2; ++j)
-      if (o_at[j] >= 0) store_codes(o + o_at[j], 1, make_float2(ko[j].x * sc.y, ko[j].y * sc.y));
+      if (o_at[j] >= 0) store_codes(o + o_at[j], 1, ko[j], sc);
     if (lane == 0) a.k_scale[slot] = sc.x;
   } else if (write) {
     uint16_t* o = static_cast<uint16_t*>(a.kc) + slot * a.d_I;
@@ -487,16 +588,19 @@ int launch_norm_rope(const void* x, int64_t ldt, int64_t ldh, int64_t T, int H, 
       break;
     }
   }
-  // a block's row slots go to one token as far as it has heads; two passes over its heads where the blocks are many
-  const int slots = NR_THREADS / G;
+  // a block's row slots go to one token as far as it has heads; where the blocks are many, a block takes more of a
+  // token's heads, then more tokens, up to two table entries a thread
+  const int slots = NR_THREADS / G, many = 4 * sm_count();
   a.spt_log = 0;
   while ((1 << a.spt_log) < slots && (1 << a.spt_log) < H) ++a.spt_log;
   const int spt = 1 << a.spt_log, NT = slots >> a.spt_log;
   a.HB = spt;
-  while (a.HB < H && a.HB < 4 * spt && cdiv(T, NT) * cdiv(H, 2 * a.HB) >= 4 * sm_count()) a.HB *= 2;
-  const int64_t gx = cdiv(T, NT);
+  a.TB = 1;
+  while (a.HB < H && a.HB < 4 * spt && cdiv(T, NT) * cdiv(H, 2 * a.HB) >= many) a.HB *= 2;
+  while (a.HB * a.TB < 8 * spt && NT * a.TB * a.R <= 1024 && cdiv(T, 2 * a.TB * NT) * cdiv(H, a.HB) >= many) a.TB *= 2;
+  const int64_t gx = cdiv(T, NT * a.TB);
   if (gx > 0x7FFFFFFF) return LSA_ERR_UNSUPPORTED;
-  const size_t smem = static_cast<size_t>(NT) * (a.R / 2) * sizeof(float2);
+  const size_t smem = static_cast<size_t>(NT) * a.TB * (a.R / 2) * sizeof(float2) + (norm == LSA_NORM_NONE ? 0 : 8 * D);
   const dim3 g(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(H, a.HB)));
   cudaError_t e = cudaErrorInvalidValue;
   if (it == 2) {

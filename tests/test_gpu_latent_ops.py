@@ -86,6 +86,24 @@ def test_norm_rope_special_rows(norm):
         assert float(sc[0]) == 1.0 or (norm == "layer" and weighted)
 
 
+def test_codes_of_rows_whose_scale_has_no_reciprocal():
+    """Rows so small that 1 / scale overflows: zeros stay zero and the others are the scale's multiples all the same."""
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=DEV)
+    x[0, 0, ::3] = 1e-37
+    x[0, 1] = torch.finfo(torch.bfloat16).tiny * (1 + torch.arange(64, device=DEV) / 64)
+    x[1, 0] = -3e-34 * (1 + torch.arange(64, device=DEV) / 64)
+    x[2, 1, 7] = 2e-36
+    y, sc = torch.empty(3, 2, 64, dtype=torch.uint8, device=DEV), torch.empty(3, 2, device=DEV)
+    lsa.lsa_norm_rope(x, y, y_scale=sc)
+    v = y.view(torch.float8_e4m3fn).double()
+    # a scale near 2^-133 has 16 bits (2^-149 is the smallest step), so quotients are off by 2^-16 more
+    q = x.double() / sc.double()[..., None]
+    assert ((v - q).abs() <= torch.maximum(q.abs() * (2.0 ** -4 + 2.0 ** -15), torch.tensor(2.0 ** -10, device=DEV))).all()
+    want = x.double().abs().amax(-1) / 448
+    assert ((sc.double() - want)[want > 0].abs() <= 2.0 ** -149 + 2.0 ** -22 * want[want > 0]).all()
+    assert not v[x == 0].any() and bool((sc[want == 0] == 1).all())
+
+
 def test_norm_rope_strides_and_in_place():
     """A head slice of a wider projection, transposed heads, a broadcast input, and the result over the input."""
     g, T, H, D = _gen(3), 37, 6, 64
