@@ -416,10 +416,7 @@ __device__ __forceinline__ void store_pair(uint16_t* p, int far, float2 v) {
     p[far] = static_cast<uint16_t>(u >> 16);
   }
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int far, float2 v, const float2& sc) {
-  float2 f[1] = {v};
-  const float inv = tiny_row(f, sc);
-  const uint32_t u = codes2(f[0], inv);
+__device__ __forceinline__ void store_codes(uint8_t* p, int far, uint32_t u) {
   if (far == 1) {
     *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(u);
   } else {
@@ -428,120 +425,125 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int far, float2 v, const
   }
 }
 
-// A warp a token: lane i holds 16 of the row's 512 normed dims and pair i of its rotary ones, and pair i and up to four
-// other dims of the index key, so one cos and sin a lane turns both and no value moves between lanes but the sums.  A
-// step's few rows are bound by latency, a prompt's by the latency of a row over the warps that an SM holds.
+// A warp a latent row, another its index key.  Lane i of the first holds 16 of the 512 normed dims and pair i of the
+// rotary ones; lane i of the second the key's pair i and up to four of its other dims: no value moves between lanes but
+// the sums, and every load is out before the first is used.  A step's few rows are bound by that chain, a prompt's by the
+// warps that an SM holds meanwhile.  16 tokens: 1.9 us (2.9 with both rows in one warp); 8192 tokens with codes: 8.0 us,
+// 2770 GB/s (7.8 with both in one warp).
 template <bool KEYS, bool FP8>
 __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = KEYS ? static_cast<int64_t>(blockIdx.x) * 2 + (warp >> 1) : static_cast<int64_t>(blockIdx.x) * 4 + warp;
   if (t >= a.T) return;
   const int64_t slot = a.slot[t];
-  const uint16_t* p = a.a + t * a.lda;
-  const uint4 v0 = *reinterpret_cast<const uint4*>(p + 8 * lane), v1 = *reinterpret_cast<const uint4*>(p + 8 * (lane + 32));
-  const int r_at = 512 + (a.half ? lane : 2 * lane), r_far = a.half ? 32 : 1;
-  float2 r = load_pair(p + r_at, r_far);
-  // the index key: its rotary pair, and dims 2 lane, 2 lane + 1 and 64 further of the others
-  const bool turn = KEYS && a.k_off >= 0;
-  const int others = KEYS ? a.d_I - (turn ? 64 : 0) : 0;
-  const int k_at = turn ? a.k_off + (a.k_half ? lane : 2 * lane) : 0, k_far = a.k_half ? 32 : 1;
-  int o_at[2];
-  float2 kr = make_float2(0.f, 0.f), ko[2] = {kr, kr};
-  if (KEYS) {
+  const int64_t pos = a.freqs ? a.pos[t] : 0;
+  const double fr = a.freqs ? a.freqs[lane] : 0.0;
+  const bool write = slot >= 0 && slot < a.n_slots;
+  if (!KEYS || (warp & 1) == 0) {
+    const uint16_t* p = a.a + t * a.lda;
+    const uint4 v[2] = {*reinterpret_cast<const uint4*>(p + 8 * lane), *reinterpret_cast<const uint4*>(p + 8 * (lane + 32))};
+    const int r_at = 512 + (a.half ? lane : 2 * lane), r_far = a.half ? 32 : 1;
+    float2 r = load_pair(p + r_at, r_far);
+    float w[2][8];
+    if (a.a_weight) {
+      if ((reinterpret_cast<uintptr_t>(a.a_weight) & 15) == 0) {
+        #pragma unroll
+        for (int i = 0; i < 2; ++i)
+          #pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<float4*>(w[i] + 4 * q) = reinterpret_cast<const float4*>(a.a_weight)[2 * (lane + 32 * i) + q];
+      } else {
+        #pragma unroll
+        for (int i = 0; i < 2; ++i)
+          #pragma unroll
+          for (int j = 0; j < 8; ++j) w[i][j] = a.a_weight[8 * (lane + 32 * i) + j];
+      }
+    }
+    if (!write && slot != -1 && lane == 0) atomicExch(&g_append_check, 1);
+    float f[2][8];
+    unpack8(v[0], f[0]);
+    unpack8(v[1], f[1]);
+    if (a.a_weight) {
+      float s = 0.f;
+      #pragma unroll
+      for (int i = 0; i < 2; ++i)
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(f[i][j], f[i][j], s);
+      const float q = rsqrtf(warp_sum(s) * (1.f / 512.f) + a.a_eps);
+      #pragma unroll
+      for (int i = 0; i < 2; ++i)
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * q * w[i][j];
+    }
+    if (a.freqs) {
+      const float2 cs = rope_cs(pos, fr, a.mul);
+      r = make_float2(r.x * cs.x - r.y * cs.y, r.y * cs.x + r.x * cs.y);
+    }
+    if (write) {
+      uint16_t* o = a.kv + slot * 576;
+      *reinterpret_cast<uint4*>(o + 8 * lane) = pack8(f[0]);
+      *reinterpret_cast<uint4*>(o + 8 * (lane + 32)) = pack8(f[1]);
+      store_pair(o + r_at, r_far, r);
+    }
+  } else {
+    // the key's rotary pair, and dims 2 lane, 2 lane + 1 and 64 further of the others
+    const bool turn = a.k_off >= 0;
+    const int others = a.d_I - (turn ? 64 : 0);
+    const int k_at = turn ? a.k_off + (a.k_half ? lane : 2 * lane) : 0, k_far = a.k_half ? 32 : 1;
     const uint16_t* kp = a.k + t * a.ldk;
-    if (turn) kr = load_pair(kp + k_at, k_far);
+    int at[3], far[3] = {k_far, 1, 1};
+    float2 v[3], w[3], b[3];
+    at[0] = turn ? k_at : -1;
     #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int e = 2 * lane + 64 * j;
-      o_at[j] = e >= others ? -1 : turn && e >= a.k_off ? e + 64 : e;
-      if (o_at[j] >= 0) ko[j] = load_pair(kp + o_at[j], 1);
+      at[j + 1] = e >= others ? -1 : turn && e >= a.k_off ? e + 64 : e;
     }
-  }
-  float2 cs = make_float2(1.f, 0.f);
-  if (a.freqs) cs = rope_cs(a.pos[t], a.freqs[lane], a.mul);
-  float f[2][8];
-  unpack8(v0, f[0]);
-  unpack8(v1, f[1]);
-  const bool write = slot >= 0 && slot < a.n_slots;
-  if (!write && slot != -1 && lane == 0) atomicExch(&g_append_check, 1);
-  if (a.a_weight) {
-    float s = 0.f;
     #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 3; ++j) {
+      v[j] = at[j] >= 0 ? load_pair(kp + at[j], far[j]) : make_float2(0.f, 0.f);
+      w[j] = a.k_weight && at[j] >= 0 ? make_float2(a.k_weight[at[j]], a.k_weight[at[j] + far[j]]) : make_float2(1.f, 1.f);
+      b[j] = a.k_bias && at[j] >= 0 ? make_float2(a.k_bias[at[j]], a.k_bias[at[j] + far[j]]) : make_float2(0.f, 0.f);
+    }
+    const float d = static_cast<float>(a.d_I), inv_d = 1.f / d;
+    if (a.k_norm == LSA_NORM_LAYER) {
+      const float mean = mean_of(warp_sum((v[0].x + v[0].y) + (v[1].x + v[1].y) + (v[2].x + v[2].y)), d, inv_d);
       #pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(f[i][j], f[i][j], s);
-    const float q = rsqrtf(warp_sum(s) * (1.f / 512.f) + a.a_eps);
-    const bool wide = (reinterpret_cast<uintptr_t>(a.a_weight) & 15) == 0;
-    #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* w = a.a_weight + 8 * (lane + 32 * i);
-      if (wide) {
-        const float4 x = reinterpret_cast<const float4*>(w)[0], y = reinterpret_cast<const float4*>(w)[1];
-        const float g[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * q * g[j];
-      } else {
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * q * w[j];
-      }
+      for (int j = 0; j < 3; ++j)
+        if (at[j] >= 0) v[j] = make_float2(v[j].x - mean, v[j].y - mean);
     }
-  }
-  if (a.freqs) r = make_float2(r.x * cs.x - r.y * cs.y, r.y * cs.x + r.x * cs.y);
-  if (write) {
-    uint16_t* o = a.kv + slot * 576;
-    *reinterpret_cast<uint4*>(o + 8 * lane) = pack8(f[0]);
-    *reinterpret_cast<uint4*>(o + 8 * (lane + 32)) = pack8(f[1]);
-    store_pair(o + r_at, r_far, r);
-  }
-  if (!KEYS) return;
-  const float d = static_cast<float>(a.d_I), inv_d = 1.f / d;
-  if (a.k_norm == LSA_NORM_LAYER) {
-    const float mean = mean_of(warp_sum(kr.x + kr.y + ((ko[0].x + ko[0].y) + (ko[1].x + ko[1].y))), d, inv_d);
+    if (a.k_norm != LSA_NORM_NONE) {
+      const float s = fmaf(v[0].x, v[0].x, v[0].y * v[0].y) +
+                      (fmaf(v[1].x, v[1].x, v[1].y * v[1].y) + fmaf(v[2].x, v[2].x, v[2].y * v[2].y));
+      const float q = rsqrtf(warp_sum(s) * inv_d + a.k_eps);
+      #pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (at[j] >= 0) v[j] = make_float2(fmaf(v[j].x * q, w[j].x, b[j].x), fmaf(v[j].y * q, w[j].y, b[j].y));
+    }
     if (turn) {
-      kr.x -= mean;
-      kr.y -= mean;
+      const float2 cs = rope_cs(pos, fr, a.mul);
+      v[0] = make_float2(v[0].x * cs.x - v[0].y * cs.y, v[0].y * cs.x + v[0].x * cs.y);
     }
-    #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (o_at[j] >= 0) {
-        ko[j].x -= mean;
-        ko[j].y -= mean;
-      }
-  }
-  if (a.k_norm != LSA_NORM_NONE) {
-    const float s = fmaf(kr.x, kr.x, kr.y * kr.y) +
-                    (fmaf(ko[0].x, ko[0].x, ko[0].y * ko[0].y) + fmaf(ko[1].x, ko[1].x, ko[1].y * ko[1].y));
-    const float q = rsqrtf(warp_sum(s) * inv_d + a.k_eps);
-    auto apply = [&](float2& v, int at, int far) {
-      const float w0 = a.k_weight ? a.k_weight[at] : 1.f, w1 = a.k_weight ? a.k_weight[at + far] : 1.f;
-      const float b0 = a.k_bias ? a.k_bias[at] : 0.f, b1 = a.k_bias ? a.k_bias[at + far] : 0.f;
-      v = make_float2(fmaf(v.x * q, w0, b0), fmaf(v.y * q, w1, b1));
-    };
-    if (turn) apply(kr, k_at, k_far);
-    #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (o_at[j] >= 0) apply(ko[j], o_at[j], 1);
-  }
-  if (turn) kr = make_float2(kr.x * cs.x - kr.y * cs.y, kr.y * cs.x + kr.x * cs.y);
-  if (FP8) {
-    const float m = fmaxf(fmaxf(fabsf(kr.x), fabsf(kr.y)),
-                          fmaxf(fmaxf(fabsf(ko[0].x), fabsf(ko[0].y)), fmaxf(fabsf(ko[1].x), fabsf(ko[1].y))));
-    const float2 sc = row_scale(warp_max(m));
-    if (!write) return;
-    uint8_t* o = static_cast<uint8_t*>(a.kc) + slot * a.d_I;
-    if (turn) store_codes(o + k_at, k_far, kr, sc);
-    #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (o_at[j] >= 0) store_codes(o + o_at[j], 1, ko[j], sc);
-    if (lane == 0) a.k_scale[slot] = sc.x;
-  } else if (write) {
-    uint16_t* o = static_cast<uint16_t*>(a.kc) + slot * a.d_I;
-    if (turn) store_pair(o + k_at, k_far, kr);
-    #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (o_at[j] >= 0) store_pair(o + o_at[j], 1, ko[j]);
+    if (FP8) {
+      float m = 0.f;
+      #pragma unroll
+      for (int j = 0; j < 3; ++j) m = fmaxf(m, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
+      const float2 sc = row_scale(warp_max(m));
+      if (!write) return;
+      uint8_t* o = static_cast<uint8_t*>(a.kc) + slot * a.d_I;
+      const float inv = tiny_row(v, sc);
+      #pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (at[j] >= 0) store_codes(o + at[j], far[j], codes2(v[j], inv));
+      if (lane == 0) a.k_scale[slot] = sc.x;
+    } else if (write) {
+      uint16_t* o = static_cast<uint16_t*>(a.kc) + slot * a.d_I;
+      #pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (at[j] >= 0) store_pair(o + at[j], far[j], v[j]);
+    }
   }
 }
 
@@ -649,7 +651,7 @@ int launch_cache_append(const void* x, int64_t ldx, const float* x_weight, float
   a.a_eps = x_eps;
   a.k_eps = k_eps;
   a.mul = mul;
-  const int64_t grid = cdiv(T, 4);
+  const int64_t grid = cdiv(T, k ? 2 : 4);
   if (grid > 0x7FFFFFFF) return LSA_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid)), b(128);
   if (!k) return cuda_status(launch_pdl(k_cache_append<false, false>, g, b, 0, s, 0u, a));
