@@ -78,9 +78,11 @@ struct PaArgs {
   int64_t Lp;
   int nP;  // prefix blocks
   float scale_log2;
-  int2* seg;      // [items] first and last pair of an item
+  int2* seg;      // [items] first and last pair of an item; last = -2: written to out already
   float2* ws_ml;  // [slots][128] running max (log2 units), sum
   float* ws_o;    // [slots][128][512]
+  uint16_t* out;
+  float* lse;
 };
 
 // A span: the blocks that one pair walks of a tile's prefix or of one query's pages.  What depends on own_len is read
@@ -458,6 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         fresh = c.t != t;
         if (fresh) mma_commit_pair(q_empty);
       }
+      // no arrival of the other CTA may outlast this one
+      for (int i = max(n - PA_NS, 0); i < n && ok; ++i) ok = mbar_wait_cluster(&s_empty[i % PA_NS], (i / PA_NS) & 1);
     }
   } else if (warp == PA_PV_WARP) {
     // ------------------------------------------------------------------ O += P V (issued by the even CTA)
@@ -602,37 +606,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       const float lt = (ls[row] + ls[128 + row]) + (ls[64 + row] + ls[192 + row]);
       if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i - 1) / PA_NP) & 1));
       tc_fence_after();
-      const int64_t prow_i = static_cast<int64_t>(id + pair) * PA_ROWS + trow;
-      // through the warp's part of the P buffers (every product is done), 32 rows x 32 columns at a time: a store
-      // instruction writes four whole 128-byte lines in place of 32 rows' 16 bytes
+      // Through the warp's part of the P buffers (every product is done), 64 bytes of 32 rows at a time: a store
+      // instruction writes whole 64-byte pieces of eight rows in place of 32 rows' 16 bytes.
       unsigned char* stage = p_s + (warp - PA_SM_WARP) * 2048;
       const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
-      const int64_t wrow = prow_i - lane;  // the warp's first row
-      #pragma unroll 1
-      for (int k = 0; k < 8 && live_rows != 0; ++k) {
-        uint32_t o[16];
-        tmem_ld16(t_o + 16 * k, o);
-        tmem_ld_wait();
-        #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        __syncwarp();
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 8 * e + (lane >> 2);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-          if ((live_rows >> r) & 1)
-            *reinterpret_cast<uint4*>(a.ws_o + (wrow + r) * 512 + 256 * kh + 128 * ch + 16 * k + 4 * (lane & 3)) = v;
+      auto put = [&](int e, uint4 v) { *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = v; };
+      auto get = [&](int r) { return *reinterpret_cast<const uint4*>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)); };
+      const bool whole = !a.multi && seg_pos == 0 && left == 0;
+      if (whole) {
+        // the rows' only part: the result itself
+        const float inv = lt != 0.f ? 1.f / lt : 0.f;
+        #pragma unroll 1
+        for (int k = 0; k < 4 && live_rows != 0; ++k) {
+          uint32_t o[32];
+          tmem_ld32(t_o + 32 * k, o);
+          tmem_ld_wait();
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t u[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 p2 = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * j]) * inv,
+                                                              __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
+              u[j] = *reinterpret_cast<const uint32_t*>(&p2);
+            }
+            put(e, make_uint4(u[0], u[1], u[2], u[3]));
+          }
+          __syncwarp();
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 8 * e + (lane >> 2);
+            const uint4 v = get(r);
+            if ((live_rows >> r) & 1)
+              *reinterpret_cast<uint4*>(a.out + (gr - lane + r) * 512 + 256 * kh + 128 * ch + 32 * k + 8 * (lane & 3)) = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (live && kh == 0 && ch == 0 && a.lse) a.lse[gr] = lt != 0.f ? (m_used + log2f(lt)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        const int64_t prow_i = static_cast<int64_t>(id + pair) * PA_ROWS + trow;
+        #pragma unroll 1
+        for (int k = 0; k < 8 && live_rows != 0; ++k) {
+          uint32_t o[16];
+          tmem_ld16(t_o + 16 * k, o);
+          tmem_ld_wait();
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) put(e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+          __syncwarp();
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 8 * e + (lane >> 2);
+            const uint4 v = get(r);
+            if ((live_rows >> r) & 1)
+              *reinterpret_cast<uint4*>(a.ws_o + (prow_i - lane + r) * 512 + 256 * kh + 128 * ch + 16 * k + 4 * (lane & 3)) = v;
+          }
+          __syncwarp();
+        }
+        if (live && kh == 0 && ch == 0) a.ws_ml[prow_i] = make_float2(m_used, lt);
       }
       tc_fence_before();
       named_bar_sync(1, 32 * PA_SM_WARPS);  // the next block's probabilities go to the same buffers
-      if (live && kh == 0 && ch == 0) a.ws_ml[prow_i] = make_float2(m_used, lt);
       if (rank == 0 && ch == 0 && L == 0) {
         if (seg_pos == 0) a.seg[id].x = pair;
-        if (left == 0) a.seg[id].y = pair;
+        if (left == 0) a.seg[id].y = whole ? -2 : pair;
       }
       m_used = -INFINITY;
       l = 0.f;
@@ -651,47 +687,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
-  cluster_sync_all();  // the other CTA's products and arrivals end here too
+  cluster_sync_relaxed();  // the other CTA's products and arrivals end here too
   if (warp == PA_PV_WARP) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
 }
 
-// One block a row (b, h): its partials, from the pairs that shared the row's items, joined by their maxima and sums.
-// G groups of 128 threads take the partials in turn (four columns a thread), the weights are formed once a block: a row
-// behind a long prefix has up to 74 partials and few other rows to hide its loads behind.
+// The partials of a row (b, h), from the pairs that shared the row's items, joined by their maxima and sums.
+struct RowParts {
+  int i0, i1, x0, x1, n0, n;  // items, their first pairs, partials of the first, of both
+  bool done;                  // written by the attention itself
+  __device__ __forceinline__ void find(const PaArgs& a, uint32_t r) {
+    const uint32_t h = static_cast<uint32_t>(a.H);
+    const int b = static_cast<int>(r / h), t = static_cast<int>(r / PA_ROWS);
+    const int qlo = static_cast<int>(static_cast<uint32_t>(t) * PA_ROWS / h);
+    // (written for items that have blocks, so the loads need not wait for the length)
+    i0 = a.multi ? qlo + 2 * t : t;
+    i1 = a.multi ? b + 2 * t + 1 : t;
+    const int2 g0 = a.seg[i0], g1 = a.seg[i1];
+    const int ob = Cursor::blocks_of(a, b);
+    x0 = g0.x;
+    x1 = g1.x;
+    const bool any = (a.multi ? a.nP : a.nP + ob) > 0;
+    done = any && g0.y == -2;
+    n0 = any ? max(g0.y - g0.x + 1, 0) : 0;
+    n = min(n0 + (a.multi && ob > 0 ? max(g1.y - g1.x + 1, 0) : 0), 2 * PA_PAIRS);
+  }
+  __device__ __forceinline__ int64_t row(int i, uint32_t r) const {
+    return static_cast<int64_t>(i < n0 ? i0 + x0 + i : i1 + x1 + i - n0) * PA_ROWS + r % PA_ROWS;
+  }
+};
+__device__ __forceinline__ uint2 pack4(const float4& v, float inv) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv), hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+__device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) {
+  if (w != 0.f) {  // a partial without keys holds nothing
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
+  }
+}
+
+// Many rows: a warp each, 16 columns a lane, a partial's maximum and sum a lane.
+__global__ void __launch_bounds__(128) k_prefix_combine_rows(const PaArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t r64 = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (r64 >= a.BH) return;
+  const uint32_t r = static_cast<uint32_t>(r64);
+  RowParts p;
+  p.find(a, r);
+  if (p.done) return;
+  float m = -INFINITY, l = 0.f;
+  float4 acc[4];
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int b0 = 0; b0 < p.n; b0 += 32) {
+    const int i = b0 + lane;
+    const float2 ml = i < p.n ? a.ws_ml[p.row(i, r)] : make_float2(0.f, 0.f);
+    const float mn = fmaxf(m, warp_max(ml.y != 0.f ? ml.x : -INFINITY));
+    const float old = m == -INFINITY ? 0.f : exp2f(m - mn), w = ml.y != 0.f ? exp2f(ml.x - mn) : 0.f;
+    m = mn;
+    l = l * old + warp_sum(w * ml.y);
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(acc[k].x * old, acc[k].y * old, acc[k].z * old, acc[k].w * old);
+    const int cnt = min(32, p.n - b0);
+    #pragma unroll 2
+    for (int j = 0; j < cnt; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float4* src = reinterpret_cast<const float4*>(a.ws_o + p.row(b0 + j, r) * 512);
+      #pragma unroll
+      for (int k = 0; k < 4; ++k) add_part(acc[k], wj, src[32 * k + lane]);
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(r) * 512)[32 * k + lane] = pack4(acc[k], inv);
+  if (a.lse && lane == 0) a.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Few rows: a block each.  G groups of 128 threads take the partials in turn (four columns a thread), the weights are
+// formed once a block: a row behind a long prefix has up to 74 partials and few other rows to hide its loads behind.
 template <int G>
-__global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint16_t* __restrict__ out,
-                                                            float* __restrict__ lse) {
-  constexpr int MAXP = 2 * PA_PAIRS, U = 6;
-  __shared__ float wt[MAXP];
+__global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a) {
+  constexpr int U = 6;
+  constexpr int ML = (2 * PA_PAIRS + 128 * G - 1) / (128 * G);  // maxima and sums a thread
+  __shared__ float wt[2 * PA_PAIRS];
   __shared__ float4 acc_s[G > 1 ? (G - 1) * 128 : 1];
   __shared__ float red[2 * 4 * G];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t r = blockIdx.x;
-  const uint32_t ur = static_cast<uint32_t>(r), uh = static_cast<uint32_t>(a.H);
-  const int b = static_cast<int>(ur / uh), t = static_cast<int>(ur / PA_ROWS), tr = static_cast<int>(ur % PA_ROWS);
-  const int qlo = static_cast<int>(static_cast<uint32_t>(t) * PA_ROWS / uh);
-  // the row's items (the first and the last pair of each; written for items that have blocks, so the loads need not
-  // wait for the length) and the number of their partials
-  const int i0 = a.multi ? qlo + 2 * t : t, i1 = a.multi ? b + 2 * t + 1 : t;
-  const int2 g0 = a.seg[i0], g1 = a.seg[i1];
-  const int ob = Cursor::blocks_of(a, b);
-  const int n0 = (a.multi ? a.nP : a.nP + ob) > 0 ? g0.y - g0.x + 1 : 0;
-  const int n1 = a.multi && ob > 0 ? g1.y - g1.x + 1 : 0;
-  const int parts = min(max(n0, 0) + max(n1, 0), MAXP);
-  auto slot_row = [&](int i) { return static_cast<int64_t>(i < n0 ? i0 + g0.x + i : i1 + g1.x + i - n0) * PA_ROWS + tr; };
+  const uint32_t r = blockIdx.x;
+  RowParts p;
+  p.find(a, r);
+  if (p.done) return;
+  const int parts = p.n;
+  auto slot_row = [&](int i) { return p.row(i, r); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = tid & 127;
-  // the maxima and sums of the parts tid and tid + 128 G, and the first of the values on their way at the same time
-  constexpr int ML = G > 1 ? 1 : 2;
+  // the parts' maxima and sums, and the first of the values on their way at the same time
   float2 ml[ML];
   #pragma unroll
-  for (int k = 0; k < ML; ++k) {
-    const int i = tid + 128 * G * k;
-    ml[k] = i < parts ? a.ws_ml[slot_row(i)] : make_float2(0.f, 0.f);
-  }
+  for (int k = 0; k < ML; ++k)
+    ml[k] = tid + 128 * G * k < parts ? a.ws_ml[slot_row(tid + 128 * G * k)] : make_float2(0.f, 0.f);
   float4 v[U];
   #pragma unroll
   for (int k = 0; k < U; ++k) {
@@ -710,9 +811,8 @@ __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint
   float l = 0.f;
   #pragma unroll
   for (int k = 0; k < ML; ++k) {
-    const int i = tid + 128 * G * k;
     const float w = ml[k].y != 0.f ? exp2f(ml[k].x - m) : 0.f;
-    if (i < parts) wt[i] = w;
+    if (tid + 128 * G * k < parts) wt[tid + 128 * G * k] = w;
     l += w * ml[k].y;
   }
   l = warp_sum(l);
@@ -732,13 +832,7 @@ __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint
     #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int i = i0k + G * k;
-      const float w = i < parts ? wt[i] : 0.f;
-      if (w != 0.f) {  // a partial without keys holds nothing
-        acc.x += w * v[k].x;
-        acc.y += w * v[k].y;
-        acc.z += w * v[k].z;
-        acc.w += w * v[k].w;
-      }
+      add_part(acc, i < parts ? wt[i] : 0.f, v[k]);
       v[k] = nx[k];
     }
   }
@@ -747,22 +841,10 @@ __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a, uint
     __syncthreads();
     if (tid >= 128) return;
     #pragma unroll
-    for (int g = 0; g < G - 1; ++g) {
-      const float4 v = acc_s[g * 128 + tid];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-    }
+    for (int g = 0; g < G - 1; ++g) add_part(acc, 1.f, acc_s[g * 128 + tid]);
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  uint2 pk;
-  pk.x = *reinterpret_cast<const uint32_t*>(&lo);
-  pk.y = *reinterpret_cast<const uint32_t*>(&hi);
-  reinterpret_cast<uint2*>(out + r * 512)[tid] = pk;
-  if (lse && tid == 0) lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(r) * 512)[tid] = pack4(acc, l != 0.f ? 1.f / l : 0.f);
+  if (a.lse && tid == 0) a.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace
@@ -833,10 +915,12 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   a.H = H;
   a.BH = B * H;
   a.nT = static_cast<int>(p.nT);
-  a.multi = p.multi;
+  a.multi = p.multi && own_len != nullptr;
   a.Lp = Lp;
   a.nP = static_cast<int>(cdiv(Lp, PA_T));
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
   a.seg = reinterpret_cast<int2*>(base);
   a.ws_ml = reinterpret_cast<float2*>(base + p.o_ml);
   a.ws_o = reinterpret_cast<float*>(base + p.o_o);
@@ -855,8 +939,9 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   LSA_CUDA_TRY(launch_pdl(k_prefix_attn, dim3(2 * PA_PAIRS), dim3(PA_THREADS), PA_SMEM, s, 0u, tq, tk, tv, tpk, tpv, a));
   // a row has about 74 / tiles partials
   const dim3 rows(static_cast<unsigned>(a.BH));
-  return cuda_status(a.nT <= 8 ? launch_pdl(k_prefix_combine<4>, rows, dim3(512), 0, s, 0u, a, static_cast<uint16_t*>(out), lse)
-                               : launch_pdl(k_prefix_combine<1>, rows, dim3(128), 0, s, 0u, a, static_cast<uint16_t*>(out), lse));
+  if (a.nT <= 8) return cuda_status(launch_pdl(k_prefix_combine<4>, rows, dim3(512), 0, s, 0u, a));
+  if (a.nT <= PA_PAIRS / 2) return cuda_status(launch_pdl(k_prefix_combine<1>, rows, dim3(128), 0, s, 0u, a));
+  return cuda_status(launch_pdl(k_prefix_combine_rows, dim3(static_cast<unsigned>(cdiv(a.BH, 4))), dim3(128), 0, s, 0u, a));
 }
 
 // The kernel's flags, read and cleared: give-up and device check; -1: CUDA error.

@@ -73,5 +73,10 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
+// the cluster's barrier without the wait for this thread's earlier stores: for an end where nothing is read any more
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 }  // namespace sm100
 }  // namespace lsa
