@@ -21,6 +21,7 @@ LSA_BF16 = 0
 LSA_FP8_E4M3 = 1
 LSA_OP_TOPK, LSA_OP_BUCKET, LSA_OP_ATTN, LSA_OP_REFINE, LSA_OP_BUCKET_MIN, LSA_OP_HYBRID_ATTN = 1, 2, 3, 4, 5, 6
 
+_bf16, _f32, _f64, _i64, _i32 = torch.bfloat16, torch.float32, torch.float64, torch.int64, torch.int32
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
 _LAYOUTS = {"interleaved": 0, "half": 1}
 _SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
@@ -318,14 +319,24 @@ def _bad(fn: str, what: str):
     raise LsaError(fn, -1, what)
 
 
-def _vec(fn: str, name: str, t, dtype, shape, dev: int):
-    """Address of an optional contiguous tensor of this dtype and shape on GPU `dev`."""
-    if t is None:
-        return None
+def _refuse(fn: str, name: str, t, dtype, shape, dev: int):
+    _bad(fn, f"{name}: contiguous {dtype} {tuple(shape)} on cuda:{dev} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _ten(fn: str, name: str, t, dtype, shape, dev: int):
+    """Address of a contiguous tensor of this dtype and shape on GPU `dev`."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    raise LsaError(fn, -1, f"{name}: contiguous {dtype} {tuple(shape)} on cuda:{dev} wanted, got {t.dtype} "
-                           f"{tuple(t.shape)} on {t.device}")
+    _refuse(fn, name, t, dtype, shape, dev)
+
+
+def _vec(fn: str, name: str, t, dtype, n: int, dev: int):
+    """Address of an optional contiguous vector of n elements."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n and t.dim() == 1 and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(fn, name, t, dtype, (n,), dev)
 
 
 def _code(fn: str, name: str, table: dict, key) -> int:
@@ -360,13 +371,13 @@ def lsa_norm_rope(x, y, pos=None, freqs=None, norm="none", weight=None, bias=Non
     """y[t, h] = norm of x[t, h] with dims [rope_off, rope_off + 2 len(freqs)) rotated by pos[t]; x bf16 [T, H, D] with
     any token and head strides, y bf16 (it may be x) or, with y_scale [T, H], e4m3 codes."""
     fn = "lsa_norm_rope"
-    if x.dim() != 3 or not x.is_cuda or x.dtype is not torch.bfloat16:
+    if x.dim() != 3 or not x.is_cuda or x.dtype is not _bf16:
         _bad(fn, "x: bf16 [T, H, D] on a GPU wanted")
     if _off_device(x):
         with torch.cuda.device(x.device):
             return lsa_norm_rope(x, y, pos, freqs, norm, weight, bias, eps, rope_off, layout, mul, y_scale, stream)
     T, H, D = shape = x.shape
-    dev, f32 = x.get_device(), torch.float32
+    dev = x.get_device()
     if y.shape != shape or y.get_device() != dev:
         _bad(fn, "y: the shape and device of x wanted")
     (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
@@ -387,18 +398,19 @@ def lsa_norm_rope(x, y, pos=None, freqs=None, norm="none", weight=None, bias=Non
         R = 2 * freqs.shape[0]
     elif pos is not None:
         _bad(fn, "pos without freqs")
-    st = load_library().lsa_norm_rope(
-        x.data_ptr(), xt, xh, T, H, D, _code(fn, "norm", _NORMS, norm), _vec(fn, "weight", weight, f32, (D,), dev),
-        _vec(fn, "bias", bias, f32, (D,), dev), eps, _vec(fn, "freqs", freqs, torch.float64, (R // 2,), dev), rope_off, R,
-        _code(fn, "layout", _LAYOUTS, layout), mul, _vec(fn, "pos", pos, torch.int64, (T,), dev), y.data_ptr(), yt, yh,
-        _dtype_code(y), _vec(fn, "y_scale", y_scale, f32, (T, H), dev), _raw_stream(stream, dev))
+    st = (_lib or load_library()).lsa_norm_rope(
+        x.data_ptr(), xt, xh, T, H, D, _code(fn, "norm", _NORMS, norm), _vec(fn, "weight", weight, _f32, D, dev),
+        _vec(fn, "bias", bias, _f32, D, dev), eps, _vec(fn, "freqs", freqs, _f64, R // 2, dev), rope_off, R,
+        _code(fn, "layout", _LAYOUTS, layout), mul, _vec(fn, "pos", pos, _i64, T, dev), y.data_ptr(), yt, yh,
+        _dtype_code(y), None if y_scale is None else _ten(fn, "y_scale", y_scale, _f32, (T, H), dev),
+        _raw_stream(stream, dev))
     if st:
         _check(fn, st)
 
 
 def _rows(fn: str, name: str, t, T, D, dev: int) -> int:
     """Row stride of bf16 [T, D] with contiguous rows."""
-    if t.shape == (T, D) and t.dtype is torch.bfloat16 and t.get_device() == dev:
+    if t.shape == (T, D) and t.dtype is _bf16 and t.get_device() == dev:
         st, sd = t.stride()
         if sd == 1:
             return st if T > 1 else 0
@@ -417,8 +429,7 @@ def lsa_cache_append(a, kv, slot, pos=None, freqs=None, kv_weight=None, kv_eps=1
         with torch.cuda.device(a.device):
             return lsa_cache_append(a, kv, slot, pos, freqs, kv_weight, kv_eps, layout, mul, k, k_cache, k_scale, k_norm,
                                     k_weight, k_bias, k_eps, k_rope_off, k_layout, stream)
-    dev, f32, bf = a.get_device(), torch.float32, torch.bfloat16
-    T, n = slot.shape[0], kv.shape[0]
+    dev, T, n = a.get_device(), slot.shape[0], kv.shape[0]
     if (freqs is None) != (pos is None) or (k is None) != (k_cache is None):
         _bad(fn, "freqs and pos, and k and k_cache, belong together")
     a_ld = _rows(fn, "a", a, T, 576, dev)
@@ -428,17 +439,16 @@ def lsa_cache_append(a, kv, slot, pos=None, freqs=None, kv_weight=None, kv_eps=1
             _bad(fn, "k [T, d_I] wanted")
         d_I, k_dtype = k.shape[1], _dtype_code(k_cache)
         k_p, k_ld = k.data_ptr(), _rows(fn, "k", k, T, d_I, dev)
-        kc_p = _vec(fn, "k_cache", k_cache, k_cache.dtype, (n, d_I), dev)
+        kc_p = _ten(fn, "k_cache", k_cache, k_cache.dtype, (n, d_I), dev)
     else:
         k_rope_off = -1
-    st = load_library().lsa_cache_append(
-        a.data_ptr(), a_ld, T, 576, 512, _vec(fn, "kv_weight", kv_weight, f32, (512,), dev), kv_eps,
-        _vec(fn, "freqs", freqs, torch.float64, (32,), dev), _code(fn, "layout", _LAYOUTS, layout), mul,
-        _vec(fn, "pos", pos, torch.int64, (T,), dev), _vec(fn, "slot", slot, torch.int64, (T,), dev),
-        _vec(fn, "kv", kv, bf, (n, 576), dev), n, k_p, k_ld, d_I, _code(fn, "k_norm", _NORMS, k_norm),
-        _vec(fn, "k_weight", k_weight, f32, (d_I,), dev), _vec(fn, "k_bias", k_bias, f32, (d_I,), dev), k_eps, k_rope_off,
-        _code(fn, "k_layout", _LAYOUTS, k_layout), kc_p, k_dtype, _vec(fn, "k_scale", k_scale, f32, (n,), dev),
-        _raw_stream(stream, dev))
+    st = (_lib or load_library()).lsa_cache_append(
+        a.data_ptr(), a_ld, T, 576, 512, _vec(fn, "kv_weight", kv_weight, _f32, 512, dev), kv_eps,
+        _vec(fn, "freqs", freqs, _f64, 32, dev), _code(fn, "layout", _LAYOUTS, layout), mul,
+        _vec(fn, "pos", pos, _i64, T, dev), _vec(fn, "slot", slot, _i64, T, dev), _ten(fn, "kv", kv, _bf16, (n, 576), dev), n,
+        k_p, k_ld, d_I, _code(fn, "k_norm", _NORMS, k_norm), _vec(fn, "k_weight", k_weight, _f32, d_I, dev),
+        _vec(fn, "k_bias", k_bias, _f32, d_I, dev), k_eps, k_rope_off, _code(fn, "k_layout", _LAYOUTS, k_layout), kc_p,
+        k_dtype, _vec(fn, "k_scale", k_scale, _f32, n, dev), _raw_stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -456,16 +466,20 @@ def lsa_prefix_attn(q, prefix, scale, out, lse=None, pages=None, table=None, own
     if _off_device(q):
         with torch.cuda.device(q.device):
             return lsa_prefix_attn(q, prefix, scale, out, lse, pages, table, own_len, ws, stream)
-    dev, bf, i32 = q.get_device(), torch.bfloat16, torch.int32
-    B, H, d_qk = q.shape
-    d_v = out.shape[2]
-    Lp = 0 if prefix is None else prefix.shape[0]
+    dev = q.get_device()
+    B, H, d_qk = q_shape = q.shape
+    d_v, Lp, prefix_p = out.shape[2], 0, None
+    if prefix is not None:
+        Lp = prefix.shape[0]
+        prefix_p = _ten(fn, "prefix", prefix, _bf16, (Lp, d_qk), dev)
     n_pages = page = cols = 0
+    pages_p = table_p = None
     if own_len is not None:
         if pages is None or table is None or pages.dim() != 3 or table.dim() != 2:
             _bad(fn, "pages [n_pages, page, 576] and table [B, cols] wanted with own_len")
         n_pages, page, _ = pages.shape
         cols = table.shape[1]
+        pages_p, table_p = _ten(fn, "pages", pages, _bf16, (n_pages, page, d_qk), dev), _ten(fn, "table", table, _i32, (B, cols), dev)
     elif pages is not None or table is not None:
         _bad(fn, "pages and table without own_len")
     ws_p = ws_n = 0
@@ -473,12 +487,10 @@ def lsa_prefix_attn(q, prefix, scale, out, lse=None, pages=None, table=None, own
         if ws.get_device() != dev or not ws.is_contiguous():
             _bad(fn, "ws: contiguous bytes on the GPU of q wanted")
         ws_p, ws_n = ws.data_ptr(), ws.numel() * ws.element_size()
-    st = load_library().lsa_prefix_attn(
-        _vec(fn, "q", q, bf, (B, H, d_qk), dev), B, H, d_qk, d_v, _vec(fn, "prefix", prefix, bf, (Lp, d_qk), dev), Lp,
-        _vec(fn, "pages", pages, bf, (n_pages, page, d_qk), dev), n_pages, page,
-        _vec(fn, "table", table, i32, (B, cols), dev), cols, _vec(fn, "own_len", own_len, i32, (B,), dev), scale,
-        _vec(fn, "out", out, bf, (B, H, d_v), dev), _vec(fn, "lse", lse, torch.float32, (B, H), dev), ws_p, ws_n,
-        _raw_stream(stream, dev))
+    st = (_lib or load_library()).lsa_prefix_attn(
+        _ten(fn, "q", q, _bf16, q_shape, dev), B, H, d_qk, d_v, prefix_p, Lp, pages_p, n_pages, page, table_p, cols,
+        _vec(fn, "own_len", own_len, _i32, B, dev), scale, _ten(fn, "out", out, _bf16, (B, H, d_v), dev),
+        None if lse is None else _ten(fn, "lse", lse, _f32, (B, H), dev), ws_p, ws_n, _raw_stream(stream, dev))
     if st:
         _check(fn, st)
 

@@ -315,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           ++nq;
         }
         for (int j = 0; j < 9; j += PA_KS) {
-          ok = __all_sync(0xffffffffu, mbar_spin(&k_empty[s], phase));
+          ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[s], phase));
           if (!ok) break;
           const uint32_t bar = mapa(smem_u32(&k_full[s]), 0);
           unsigned char* dst = k_s + s * PA_K_BYTES;
@@ -367,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         }
         const bool one = elect_one();
         for (int k = 0; k < PA_T && key0 + k < c.len; k += PA_VT) {
-          ok = __all_sync(0xffffffffu, mbar_spin(&v_empty[s], phase));
+          ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[s], phase));
           if (!ok) break;
           unsigned char* dst = v_s + s * PA_V_BYTES;
           if (c.b < 0) {
@@ -529,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       for (end = c.span(i, n); i < end; ++i, ++c.pos) {
         const int sb = i % PA_NS, pb = i % PA_NP;
         const int nvalid = len - PA_T * c.block();
-        if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&s_full[sb], (i / PA_NS) & 1));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (i / PA_NS) & 1));
         tc_fence_after();
         uint32_t sr[32];
         tmem_ld32(t_s + sb * PA_KT, sr);
@@ -565,10 +565,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           pk[k / 2] = *reinterpret_cast<const uint32_t*>(&p2);
         }
         l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-        if (i >= PA_NP && ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i / PA_NP) - 1) & 1));
+        if (i >= PA_NP && ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[pb], ((i / PA_NP) - 1) & 1));
         // O changes its reference only when a maximum grew by more than 2^8 (no product is running then)
         if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[(i - 1) % PA_NP], ((i - 1) / PA_NP) & 1));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(i - 1) % PA_NP], ((i - 1) / PA_NP) & 1));
           tc_fence_after();
           #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
@@ -604,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       named_bar_sync(1, 32 * PA_SM_WARPS);
       // one order of addition for all four threads of a row
       const float lt = (ls[row] + ls[128 + row]) + (ls[64 + row] + ls[192 + row]);
-      if (ok) ok = __all_sync(0xffffffffu, mbar_spin(&pv_done[pb], ((i - 1) / PA_NP) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[pb], ((i - 1) / PA_NP) & 1));
       tc_fence_after();
       // Through the warp's part of the P buffers (every product is done), 64 bytes of 32 rows at a time: a store
       // instruction writes whole 64-byte pieces of eight rows in place of 32 rows' 16 bytes.
