@@ -16,9 +16,12 @@
 // twice, 1088 bytes a key and CTA, the second time from L2.  Keys arrive in stages of 64 keys x 192 dims (three a
 // block) and values in stages of 32 keys, each by one instruction of a three-dimensional map: a warp that issues a load
 // waits about 200 clocks before its next, so nine small loads a block held the block at 3750 clocks.  With 64-key
-// blocks (N = 64, A read again for each, 22.6 clocks a key and SM against 17.0) the same batch took 529 us against 470 (before the walk below).
-// 16 queries of 128 heads behind 131072 rows: 398 us, 1470 TFLOP/s; 64 queries behind 32749: 399 us, 1485 TFLOP/s,
-// where the GPU's power limit holds the clock near 1.4 GHz (cuBLAS sustains 1385 there).
+// blocks (N = 64, A read again for each, 22.6 clocks a key and SM against 17.0) the decode batch below took 529 us against
+// 470, both before pairs walked in step; prefetching blocks into the L2 ahead of the loads gained nothing.
+// 16 queries of 128 heads behind 131072 rows: 400 us (1460 TFLOP/s, matrix units busy 86% of the time), 478 us when run
+// for seconds, where the power limit holds the clock (1225 TFLOP/s; cuBLAS sustains 1385 there).  64 queries behind 32749
+// rows: 405 us, 481 sustained.  One query of 128 heads behind 131072 rows: 49 us, of which 28 in the loop (5.4 TB/s from
+// HBM) and 21 in start, partials and join.  4 queries of 16 heads behind 1024 rows: 13 us, all latency.
 //
 // Work is cut evenly: the blocks of all tiles, in order, are one line that 74 pairs divide; a tile that spans pairs
 // leaves partial sums (fp32) that k_prefix_combine joins.  Where a tile holds several queries (H not a multiple of 128),
@@ -39,11 +42,8 @@ constexpr int PA_KQ_WARP = 0, PA_QK_WARP = 1, PA_PV_WARP = 2, PA_V_WARP = 3, PA_
 constexpr int PA_PAIRS = 74;  // one pair on every two of the 148 SMs
 constexpr int PA_T = 128;     // keys of a block
 constexpr int PA_ROWS = 128;  // query rows of a tile
-#ifndef PA_NK_
-#define PA_NK_ 3
-#define PA_NV_ 4
-#endif
-constexpr int PA_NK = PA_NK_, PA_NV = PA_NV_, PA_NS = 4, PA_NP = 1;
+constexpr int PA_NK = 3, PA_NV = 4;  // stages
+constexpr int PA_NS = 4, PA_NP = 1;  // buffers of S and of P
 constexpr int PA_Q_KB = 64 * 128;        // 64 rows x 64 dims
 constexpr int PA_Q_BYTES = 9 * PA_Q_KB;  // 72 KB
 constexpr int PA_P_KB = 64 * 128;        // 64 rows x 64 keys
@@ -291,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   bool ok = true;
 
   if (warp == PA_KQ_WARP) {
-    // ------------------------------------------------------------------ Q and keys: stages of 64 keys x 64 dims
+    // ------------------------------------------------------------------ Q and keys: stages of 64 keys x 192 dims
     int loaded = -1, nq = 0;
     uint32_t s = 0, phase = 1;
     for (int i = 0, end; i < n && ok;) {

@@ -146,14 +146,17 @@ struct NormRopeArgs {
 // of weights halve the warps of an SM (70 us against 45 for 8192 x 64 rows of 128 dims).  Products and sums go two an
 // instruction.  Small blocks (128 threads, six an SM) wait for each other least: 43.4 us against 44.6 at 256 threads and
 // 70 at 512; a grid of resident blocks with two tables in turn took 55.
-// 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 43.4 us, 6190 GB/s.  2047 x 128 rows of 64, no norm: 10.9 us,
-// 6170 GB/s.  4099 x 64 rows of 128, layer norm, to codes: 29.4 us, 3460 GB/s, bound by its instructions (three reductions
+// 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 45.6 us, 5890 GB/s.  2047 x 128 rows of 64, no norm, into
+// their place in rows of 1152 bytes: 17.9 us cold, 3750 GB/s (128-byte pieces of HBM pages; 11 us in the L2).  4099 x 64 rows of 128, layer norm, to codes: 29.4 us, 3460 GB/s, bound by its instructions (three reductions
 // and a scale a row, 17 operations an element).
 template <int G, int ITER, int NORM, bool FP8>
 __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(const NormRopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin | weight [D] | bias [D]
   sm100::pdl_wait();
-  sm100::pdl_launch_dependents();
+  // A bf16 result may be the query of the decode attention, which reads its query before it waits for this kernel: there
+  // the next kernel starts when every block has ended, with its stores done (2 us of 44 at 8192 x 64 rows).  Codes only go
+  // where they are waited for.
+  if (FP8) sm100::pdl_launch_dependents();
   constexpr int RPT = ITER <= 2 ? 2 : 1;
   const int slot = threadIdx.x / G, gl = threadIdx.x % G;
   const int spt = 1 << a.spt_log, NT = (NR_THREADS / G) >> a.spt_log;
@@ -365,6 +368,10 @@ __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(con
       }
     }
   }
+  if (!FP8) {
+    __syncthreads();
+    if (threadIdx.x == 0) __threadfence();  // with the barrier: the block's stores
+  }
 }
 
 template <int G, int ITER>
@@ -427,11 +434,12 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int far, uint32_t u) {
 
 // A warp a latent row, another its index key.  Lane i of the first holds 16 of the 512 normed dims and pair i of the
 // rotary ones; lane i of the second the key's pair i and up to four of its other dims: no value moves between lanes but
-// the sums, and every load is out before the first is used.  A step's few rows are bound by that chain, a prompt's by the
-// warps that an SM holds meanwhile.  16 tokens: 1.9 us (2.9 with both rows in one warp); 8192 tokens with codes: 8.0 us,
-// 2770 GB/s (7.8 with both in one warp).
+// the sums.  A step's few rows are bound by the chain of loads, sums and stores, a prompt's by the rows that an SM holds
+// meanwhile, so registers are kept to 12 blocks an SM (the weights are read when they are used).  16 tokens: 1.9 us with
+// warm caches, 3.4 us cold (2.9 warm with both rows in one warp); 8192 tokens with codes: 10.9 us cold, 2040 GB/s (12.0
+// with 9 blocks an SM).
 template <bool KEYS, bool FP8>
-__global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
+__global__ void __launch_bounds__(128, 12) k_cache_append(const AppendArgs a) {
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -446,21 +454,6 @@ __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
     const uint4 v[2] = {*reinterpret_cast<const uint4*>(p + 8 * lane), *reinterpret_cast<const uint4*>(p + 8 * (lane + 32))};
     const int r_at = 512 + (a.half ? lane : 2 * lane), r_far = a.half ? 32 : 1;
     float2 r = load_pair(p + r_at, r_far);
-    float w[2][8];
-    if (a.a_weight) {
-      if ((reinterpret_cast<uintptr_t>(a.a_weight) & 15) == 0) {
-        #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<float4*>(w[i] + 4 * q) = reinterpret_cast<const float4*>(a.a_weight)[2 * (lane + 32 * i) + q];
-      } else {
-        #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          #pragma unroll
-          for (int j = 0; j < 8; ++j) w[i][j] = a.a_weight[8 * (lane + 32 * i) + j];
-      }
-    }
     if (!write && slot != -1 && lane == 0) atomicExch(&g_append_check, 1);
     float f[2][8];
     unpack8(v[0], f[0]);
@@ -472,10 +465,20 @@ __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
         #pragma unroll
         for (int j = 0; j < 8; ++j) s = fmaf(f[i][j], f[i][j], s);
       const float q = rsqrtf(warp_sum(s) * (1.f / 512.f) + a.a_eps);
+      const bool wide = (reinterpret_cast<uintptr_t>(a.a_weight) & 15) == 0;
       #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        const float* w = a.a_weight + 8 * (lane + 32 * i);
         #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * q * w[i][j];
+        for (int p = 0; p < 2; ++p) {
+          const float4 g = wide ? *reinterpret_cast<const float4*>(w + 4 * p)
+                                : make_float4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+          f[i][4 * p] = f[i][4 * p] * q * g.x;
+          f[i][4 * p + 1] = f[i][4 * p + 1] * q * g.y;
+          f[i][4 * p + 2] = f[i][4 * p + 2] * q * g.z;
+          f[i][4 * p + 3] = f[i][4 * p + 3] * q * g.w;
+        }
+      }
     }
     if (a.freqs) {
       const float2 cs = rope_cs(pos, fr, a.mul);

@@ -389,6 +389,30 @@ def test_prefix_attn_refusals():
 # ------------------------------------------------------------------------------------------------ together
 
 
+def test_queries_rotated_right_before_the_sparse_attention():
+    """The decode attention loads its query before it waits for the kernel ahead of it: a rotation that writes the query
+    has to be over by then (new queries each time, more than one wave of blocks)."""
+    g, B, H, L, n = _gen(40), 16, 128, 4096, 24
+    kv = _randn(g, L, 576).bfloat16()
+    raw = [(2 * _randn(g, B, H, 576)).bfloat16() for _ in range(n)]
+    pos = torch.randint(0, 100000, (B,), generator=g, device=DEV)
+    freqs, _ = lsa.lsa_rope_freqs(64)
+    idx = torch.stack([torch.randperm(L, generator=g, device=DEV)[:256].sort().values for _ in range(B)]).int().contiguous()
+    cnt = torch.full((B,), 256, dtype=torch.int32, device=DEV)
+    ws = lsa.workspace(lsa.lsa_workspace_size(lsa.LSA_OP_ATTN, B, L, 256, H), DEV)
+    q, outs = torch.zeros_like(raw[0]), [torch.empty(B, H, 512, dtype=torch.bfloat16, device=DEV) for _ in range(n)]
+    for i in range(n):
+        lsa.lsa_norm_rope(raw[i], q, pos, freqs, norm="rms", rope_off=512)
+        lsa.lsa_sparse_attn(q, kv, idx, cnt, 0.04, outs[i], None, ws)
+    torch.cuda.synchronize()
+    for i in range(n):
+        lsa.lsa_norm_rope(raw[i], q, pos, freqs, norm="rms", rope_off=512)
+        torch.cuda.synchronize()
+        want = torch.empty_like(outs[i])
+        lsa.lsa_sparse_attn(q, kv, idx, cnt, 0.04, want, None, ws)
+        assert torch.equal(outs[i], want), i
+
+
 def test_streams_graphs_and_repeats():
     """Each operator on a side stream, captured and replayed on new inputs, two graphs in flight with their own
     workspaces; the same inputs give the same bytes."""
