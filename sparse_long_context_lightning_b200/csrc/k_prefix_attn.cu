@@ -24,7 +24,8 @@
 // HBM) and 21 in start, partials and join.  4 queries of 16 heads behind 1024 rows: 13 us, all latency.
 //
 // Work is cut evenly: the blocks of all tiles, in order, are one line that 74 pairs divide; a tile that spans pairs
-// leaves partial sums (fp32) that k_prefix_combine joins.  Where a tile holds several queries (H not a multiple of 128),
+// leaves partial sums (fp32) that a second kernel joins, and one that lies in a pair is written at once (74 queries of 128
+// heads with 1000 own tokens each: 30.5 us against 50.3 through partials).  Where a tile holds several queries (H not a multiple of 128),
 // each query's own blocks are an accumulation of their own, so that a row never multiplies another sequence's values.
 #include "lsa_common.cuh"
 #include "sm100_pair.cuh"
@@ -60,6 +61,7 @@ static_assert(PA_SMEM <= 232448, "shared memory");
 constexpr uint32_t PT_O = 0, PT_S = 256;  // TMEM columns: O [0, 256), S buffers of 64 from 256
 constexpr uint32_t IDESC_QK = idesc_mma(128, PA_T, 1u, 0u);
 constexpr uint32_t IDESC_PV2 = idesc_mma(128, 256, 1u, 1u);
+constexpr int PA_END = 1;  // what an own item's end counts for when the work is cut, in blocks
 constexpr float PA_RESCALE = 8.f;
 constexpr int PA_NO_ROW = 0x7FFFFF00;  // behind every map's last row: the box reads as zeros
 
@@ -89,11 +91,16 @@ struct PaArgs {
 // once a span (a load a block cost the softmax 780 clocks of 2100).
 // Items: a tile where all rows belong to one query; else a tile's prefix part, and each of its queries' own part.
 // Their numbers rise along the line of blocks, and so does number + pair: the slot of a (item, pair) partial.
+// The line counts units: a block is one, and the end of a query's own item (its last products awaited, its rows stored)
+// counts for PA_END more: 45.3 -> 42.2 us for 33 queries of 32 heads with up to 2000 own tokens (2 units: 41.1 there, but
+// 15.2 -> 15.9 where the items are one block each).
 struct Cursor {
   int t, b;  // tile; query whose own blocks are walked, or -1: the prefix
-  int pos, cnt;
-  int len;  // keys of the prefix or of the query's pages
-  int turn, wrap, width;  // of the span: where the walk begins
+  int pos, cnt;  // units
+  int len;       // keys of the prefix or of the query's pages
+  int blocks;    // of the prefix or of the query's pages: the units that are blocks
+  int real;      // blocks of the span
+  int turn, wrap;  // of the span: where the walk begins
   int qlo, qhi;
 
   static __device__ __forceinline__ int len_of(const PaArgs& a, int b) {
@@ -101,27 +108,31 @@ struct Cursor {
     return min(max(__ldg(a.own_len + b), 0), a.cap);
   }
   static __device__ __forceinline__ int blocks_of(const PaArgs& a, int b) { return (len_of(a, b) + PA_T - 1) / PA_T; }
+  static __device__ __forceinline__ int units(const PaArgs& a, int blocks) {  // of an own part
+    return blocks + (a.multi && blocks > 0 ? PA_END : 0);
+  }
   __device__ __forceinline__ void tile(const PaArgs& a, int tt) {
     t = tt;
     b = -1;
-    cnt = a.nP;
+    cnt = blocks = a.nP;
     len = static_cast<int>(a.Lp);
     const uint32_t r0 = static_cast<uint32_t>(tt) * PA_ROWS, h = static_cast<uint32_t>(a.H);  // rows fit 31 bits
     qlo = static_cast<int>(r0 / h);
     qhi = static_cast<int>((min(r0 + PA_ROWS, static_cast<uint32_t>(a.BH)) - 1) / h);
   }
-  __device__ __forceinline__ void settle(const PaArgs& a) {  // to the block that `pos` counts up to; one must be left
+  __device__ __forceinline__ void settle(const PaArgs& a) {  // to the unit that `pos` counts up to; one must be left
     while (pos >= cnt) {
       pos -= cnt;
       b = b < 0 ? qlo : b + 1;
       if (b <= qhi) {
         len = len_of(a, b);
-        cnt = (len + PA_T - 1) / PA_T;
+        blocks = (len + PA_T - 1) / PA_T;
+        cnt = units(a, blocks);
       } else if (t + 1 < a.nT) {
         tile(a, t + 1);
       } else {  // not reached unless own_len changed since the blocks were counted: rows outside the maps, zeros
         b = -1;
-        cnt = 0x7FFFFFFF;
+        cnt = blocks = 0x7FFFFFFF;
       }
     }
   }
@@ -130,43 +141,46 @@ struct Cursor {
     pos = off;
     settle(a);
   }
-  // The span's end among the pair's n blocks, of which i are done.  A prefix span is walked from the block that is i
-  // modulo n, and round: pairs at the same i then read the same few places of the prefix whichever tile they work on, so
-  // that a prefix larger than the L2 comes from HBM about once (n differs by one block between pairs at most): 16 queries
-  // of 128 heads behind 131072 rows (151 MB) 458 -> 398 us.
-  __device__ __forceinline__ int span(int i, int n) {
-    const int w = min(n - i, cnt - pos);
+  // The units of the span that begins after u of the pair's n, and its blocks (`real`).  A prefix span is walked from the
+  // block that is u modulo n, and round: pairs at the same u then read the same few places of the prefix whichever tile
+  // they work on, so that a prefix larger than the L2 comes from HBM about once (n differs by one between pairs at most):
+  // 16 queries of 128 heads behind 131072 rows (151 MB) 458 -> 398 us.
+  __device__ __forceinline__ int span(int u, int n) {
+    const int w = min(n - u, cnt - pos);
+    real = min(w, max(blocks - pos, 0));
     turn = 0;
     wrap = 0x7FFFFFFF;
-    width = w;
     if (b < 0) {
-      int r = (i - pos) % n;
+      int r = (u - pos) % n;
       if (r < 0) r += n;
-      if (r < w) {
+      if (r < real) {
         turn = r;
-        wrap = pos + w;
+        wrap = pos + real;
       }
     }
-    return i + w;
+    return w;
   }
   __device__ __forceinline__ int block() const {
     const int x = pos + turn;
-    return x >= wrap ? x - width : x;
+    return x >= wrap ? x - real : x;
   }
   __device__ __forceinline__ int id(const PaArgs& a) const {
     return !a.multi ? t : (b < 0 ? qlo + 2 * t : b + 2 * t + 1);
   }
+  // blocks of the item before `pos`, and behind it
   __device__ __forceinline__ int item_pos(const PaArgs& a) const { return a.multi || b < 0 ? pos : a.nP + pos; }
-  __device__ __forceinline__ int item_cnt(const PaArgs& a) const { return a.multi ? cnt : a.nP + blocks_of(a, qlo); }
+  __device__ __forceinline__ int item_left(const PaArgs& a) const {
+    return max(blocks - pos, 0) + (a.multi || b >= 0 ? 0 : blocks_of(a, qlo));
+  }
 };
 
-__device__ __forceinline__ int tile_blocks(const PaArgs& a, int t) {
+__device__ __forceinline__ int tile_units(const PaArgs& a, int t) {
   Cursor c;
   c.tile(a, t);
   int n = a.nP;
   if (a.own_len) {
     #pragma unroll 4
-    for (int b = c.qlo; b <= c.qhi; ++b) n += Cursor::blocks_of(a, b);
+    for (int b = c.qlo; b <= c.qhi; ++b) n += Cursor::units(a, Cursor::blocks_of(a, b));
   }
   return n;
 }
@@ -193,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   uint64_t* pv_done = p_full + PA_NP;
   uint64_t* vt_full = pv_done + PA_NP;  // this CTA's values of a stage whose last page is partly filled
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(vt_full + 1);
-  int* start_s = reinterpret_cast<int*>(tmem_holder + 1);  // this pair's first tile, block of it, number of blocks
+  int* start_s = reinterpret_cast<int*>(tmem_holder + 1);  // this pair's first tile, unit of it, number of units
   int* abort_flag = start_s + 3;
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -244,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     const int per = (a.nT + PA_THREADS - 1) / PA_THREADS;
     const int lo = min(tid * per, a.nT), hi = min(lo + per, a.nT);
     int64_t mine = 0;
-    for (int t = lo; t < hi; ++t) mine += tile_blocks(a, t);
+    for (int t = lo; t < hi; ++t) mine += tile_units(a, t);
     int64_t inc = mine;
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -271,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       if (s0 >= before && s0 < before + mine) {
         int64_t off = s0 - before;
         int t = lo;
-        for (int n = tile_blocks(a, t); off >= n && t + 1 < hi; n = tile_blocks(a, t)) {
+        for (int n = tile_units(a, t); off >= n && t + 1 < hi; n = tile_units(a, t)) {
           off -= n;
           ++t;
         }
@@ -294,17 +308,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     // ------------------------------------------------------------------ Q and keys: stages of 64 keys x 192 dims
     int loaded = -1, nq = 0;
     uint32_t s = 0, phase = 1;
-    for (int i = 0, end; i < n && ok;) {
-      for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+    // the page of this lane's box among this CTA's keys of own block p, or -1; asked for a block ahead
+    auto page_of = [&](int p) {
+      const int key = PA_T * p + PA_KT * static_cast<int>(rank) + lane * a.kbox;
+      return lane * a.kbox < PA_KT && key < c.len ? a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)] : -1;
+    };
+    for (int u = 0; u < n && ok;) {
+      const int w = c.span(u, n), end = c.pos + c.real;
+      int pg_next = c.b >= 0 && c.real > 0 ? page_of(c.pos) : -1;
+      for (; c.pos < end && ok; ++c.pos) {
         const int key0 = PA_T * c.block() + PA_KT * static_cast<int>(rank);
-        // page rows of this CTA's keys (lane = box); a box past the end reads as zeros: a row outside the map
+        // a box past the end reads as zeros: a row outside the map
         int y = PA_NO_ROW;
         if (c.b >= 0) {
-          const int key = key0 + lane * a.kbox;
-          if (lane * a.kbox < PA_KT && key < c.len) {
-            const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
-            if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-          }
+          const int pg = pg_next;
+          if (c.pos + 1 < end) pg_next = page_of(c.pos + 1);
+          if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + ((key0 + lane * a.kbox) & ((1 << a.page_shift) - 1));
         }
         const bool one = elect_one();
         const bool fresh = c.t != loaded;
@@ -347,82 +366,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           }
         }
       }
-      if (i < n && ok) c.settle(a);
+      c.pos += w - c.real;
+      u += w;
+      if (u < n && ok) c.settle(a);
     }
   } else if (warp == PA_V_WARP) {
     // ------------------------------------------------------------------ values: this CTA's 256 dims, stages of 32 keys
-    int ntail = 0;
+    int ntail = 0, tail_s = -1, tail_valid = 0;
     uint32_t s = 0, phase = 1;
-    for (int i = 0, end; i < n && ok;) {
-      for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+    auto page_of = [&](int p) {
+      const int key = PA_T * p + lane * a.vbox;
+      return lane * a.vbox < PA_T && key < c.len ? a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)] : 0;
+    };
+    // Rows of a partly filled box behind the sequence's end hold anything (NaN too) and would meet p = 0 in the product:
+    // such a stage lands on this CTA's own barrier, and before this warp next waits for a free stage it zeroes the rows
+    // and hands the stage over.
+    auto hand_over = [&]() {
+      ok = __all_sync(0xffffffffu, mbar_wait(vt_full, ntail & 1));
+      if (!ok) return;
+      ++ntail;
+      unsigned char* dst = v_s + tail_s * PA_V_BYTES;
+      const int rows = (tail_valid + a.vbox - 1) / a.vbox * a.vbox - tail_valid;
+      for (int x = lane; x < 4 * rows * 8; x += 32) {
+        const int j = x / (rows * 8), e = x - j * rows * 8;
+        *reinterpret_cast<uint4*>(dst + j * PA_V_KB + tail_valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (elect_one()) mbar_arrive_pair(mapa(smem_u32(&v_full[tail_s]), 0));
+      __syncwarp();
+      tail_s = -1;
+    };
+    for (int u = 0; u < n && ok;) {
+      const int w = c.span(u, n), end = c.pos + c.real;
+      int pg_next = c.b >= 0 && c.real > 0 ? page_of(c.pos) : 0;
+      for (; c.pos < end && ok; ++c.pos) {
         const int key0 = PA_T * c.block();
         int y = PA_NO_ROW;
         if (c.b >= 0) {
-          const int key = key0 + lane * a.vbox;
+          const int pg = pg_next, key = key0 + lane * a.vbox;
+          if (c.pos + 1 < end) pg_next = page_of(c.pos + 1);
           if (lane * a.vbox < PA_T && key < c.len) {
-            const int pg = a.table[static_cast<int64_t>(c.b) * a.table_ld + (key >> a.page_shift)];
             if (pg >= 0 && pg < a.n_pages) y = (pg << a.page_shift) + (key & ((1 << a.page_shift) - 1));
             else atomicExch(&g_prefix_check, 1);
           }
         }
         const bool one = elect_one();
         for (int k = 0; k < PA_T && key0 + k < c.len; k += PA_VT) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[s], phase));
+          const int valid = min(PA_VT, c.len - key0 - k);
+          const bool tail = c.b >= 0 && (valid & (a.vbox - 1)) != 0;
+          if (tail_s >= 0 && (tail || !__all_sync(0xffffffffu, mbar_test_wait(&v_empty[s], phase)))) hand_over();
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&v_empty[s], phase));
           if (!ok) break;
           unsigned char* dst = v_s + s * PA_V_BYTES;
+          if (one) {
+            if (tail) mbar_expect_tx(vt_full, PA_V_BYTES);
+            else if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
+            else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
+          }
+          __syncwarp();
+          const uint32_t bar = tail ? mapa(smem_u32(vt_full), rank) : mapa(smem_u32(&v_full[s]), 0);
           if (c.b < 0) {
-            if (one) {
-              if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
-              else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
-              const uint32_t bar = mapa(smem_u32(&v_full[s]), 0);
-              tma_load_3d_pair(dst, &tm_v, bar, 0, key0 + k, 4 * static_cast<int>(rank));
-            }
+            if (one) tma_load_3d_pair(dst, &tm_v, bar, 0, key0 + k, 4 * static_cast<int>(rank));
+          } else if (a.vbox == PA_VT) {
+            const int y0 = __shfl_sync(0xffffffffu, y, k / PA_VT);
+            if (one) tma_load_3d_pair(dst, &tm_pv, bar, 0, y0, 4 * static_cast<int>(rank));
           } else {
-            // rows of a partly filled box behind the sequence's end hold anything (NaN too) and would meet p = 0 in the
-            // product: such a stage lands on this CTA's own barrier, has those rows zeroed, and is then handed over
-            const int valid = min(PA_VT, c.len - key0 - k);
-            const bool tail = (valid & (a.vbox - 1)) != 0;
-            const uint32_t bar = tail ? mapa(smem_u32(vt_full), rank) : mapa(smem_u32(&v_full[s]), 0);
-            if (one) {
-              if (tail) mbar_expect_tx(vt_full, PA_V_BYTES);
-              else if (rank == 0) mbar_expect_tx(&v_full[s], 2 * PA_V_BYTES);
-              else mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
-            }
-            __syncwarp();
-            if (a.vbox == PA_VT) {
-              const int y0 = __shfl_sync(0xffffffffu, y, k / PA_VT);
-              if (one) tma_load_3d_pair(dst, &tm_pv, bar, 0, y0, 4 * static_cast<int>(rank));
-            } else {
-              for (int r = 0; r * a.vbox < PA_VT; ++r) {
-                const int yr = __shfl_sync(0xffffffffu, y, k / a.vbox + r);
-                if (one)
-                  for (int j = 0; j < 4; ++j)
-                    tma_load_3d_pair(dst + j * PA_V_KB + r * a.vbox * 128, &tm_pv, bar, 0, yr, 4 * static_cast<int>(rank) + j);
-              }
-            }
-            if (tail) {
-              ok = __all_sync(0xffffffffu, mbar_wait(vt_full, ntail & 1));
-              if (!ok) break;
-              ++ntail;
-              const int rows = (valid + a.vbox - 1) / a.vbox * a.vbox - valid;
-              for (int x = lane; x < 4 * rows * 8; x += 32) {
-                const int j = x / (rows * 8), e = x - j * rows * 8;
-                *reinterpret_cast<uint4*>(dst + j * PA_V_KB + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (one) mbar_arrive_pair(mapa(smem_u32(&v_full[s]), 0));
+            for (int r = 0; r * a.vbox < PA_VT; ++r) {
+              const int yr = __shfl_sync(0xffffffffu, y, k / a.vbox + r);
+              if (one)
+                for (int j = 0; j < 4; ++j)
+                  tma_load_3d_pair(dst + j * PA_V_KB + r * a.vbox * 128, &tm_pv, bar, 0, yr, 4 * static_cast<int>(rank) + j);
             }
           }
           __syncwarp();
+          if (tail) {
+            tail_s = static_cast<int>(s);
+            tail_valid = valid;
+          }
           if (++s == PA_NV) {
             s = 0;
             phase ^= 1;
           }
         }
       }
-      if (i < n && ok) c.settle(a);
+      c.pos += w - c.real;
+      u += w;
+      if (u < n && ok) c.settle(a);
     }
+    if (tail_s >= 0 && ok) hand_over();
   } else if (warp == PA_QK_WARP) {
     // ------------------------------------------------------------------ S = Q K^T (issued by the even CTA)
     if (rank == 0 && n > 0 && elect_one()) {
@@ -430,8 +462,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       int nq = 0;
       bool fresh = true;
       uint32_t s = 0, phase = 0;
-      for (int i = 0, end; i < n && ok;) {
-        for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+      int i = 0;
+      for (int u = 0; u < n && ok;) {
+        const int w = c.span(u, n);
+        for (const int end = i + c.real; i < end && ok; ++i, ++c.pos) {
           const int sb = i % PA_NS;
           ok = ok && mbar_wait_cluster(&s_empty[sb], ((i / PA_NS) & 1) ^ 1);
           #pragma unroll
@@ -454,14 +488,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           if (fresh) ++nq;
           fresh = false;
         }
-        if (i >= n || !ok) break;
+        c.pos += w - c.real;
+        u += w;
+        if (u >= n || !ok) break;
         const int t = c.t;
         c.settle(a);
-        fresh = c.t != t;
-        if (fresh) mma_commit_pair(q_empty);
+        if (c.t != t && !fresh) {  // (a tile of which this pair had no block brought no queries)
+          fresh = true;
+          mma_commit_pair(q_empty);
+        }
       }
       // no arrival of the other CTA may outlast this one
-      for (int i = max(n - PA_NS, 0); i < n && ok; ++i) ok = mbar_wait_cluster(&s_empty[i % PA_NS], (i / PA_NS) & 1);
+      for (int j = max(i - PA_NS, 0); j < i && ok; ++j) ok = mbar_wait_cluster(&s_empty[j % PA_NS], (j / PA_NS) & 1);
     }
   } else if (warp == PA_PV_WARP) {
     // ------------------------------------------------------------------ O += P V (issued by the even CTA)
@@ -469,10 +507,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       const uint64_t pdesc = desc_sw128(smem_u32(p_s)), vdesc = desc_sw128_mn(smem_u32(v_s), PA_V_KB, 1024);
       int item = -1;
       uint32_t s = 0, phase = 0;
-      for (int i = 0, end; i < n && ok;) {
+      for (int u = 0, i = 0; u < n && ok;) {
         uint32_t acc = c.id(a) == item;
         item = c.id(a);
-        for (end = c.span(i, n); i < end && ok; ++i, ++c.pos) {
+        const int w = c.span(u, n);
+        for (const int end = i + c.real; i < end && ok; ++i, ++c.pos) {
           const int pb = i % PA_NP;
           ok = mbar_wait_cluster(&p_full[pb], (i / PA_NP) & 1);
           #pragma unroll
@@ -498,7 +537,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
           }
           if (ok) mma_commit_pair(&pv_done[pb]);
         }
-        if (i < n && ok) c.settle(a);
+        c.pos += w - c.real;
+        u += w;
+        if (u < n && ok) c.settle(a);
       }
     }
   } else if (n > 0) {
@@ -520,13 +561,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     float m_used = -INFINITY, l = 0.f;
     bool first = true;
     int seg_pos = c.item_pos(a);
-    for (int i = 0, end; i < n;) {
+    for (int u = 0, i = 0; u < n;) {
       // whether this thread's row is one of the span's
       const int64_t gr = static_cast<int64_t>(c.t) * PA_ROWS + trow;
       const bool live = gr < a.BH && (!a.multi || c.b < 0 || (gr >= static_cast<int64_t>(c.b) * a.H &&
                                                               gr < static_cast<int64_t>(c.b + 1) * a.H));
       const int len = live ? c.len - 64 * kh - 32 * ch : 0;
-      for (end = c.span(i, n); i < end; ++i, ++c.pos) {
+      const int w = c.span(u, n);
+      for (const int end = i + c.real; i < end; ++i, ++c.pos) {
         const int sb = i % PA_NS, pb = i % PA_NP;
         const int nvalid = len - PA_T * c.block();
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (i / PA_NS) & 1));
@@ -592,10 +634,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         if (lane == 0) mbar_arrive_pair(c_p_full + 8 * pb);
         first = false;
       }
-      const int id = c.id(a), left = c.item_cnt(a) - c.item_pos(a);
-      if (i < n) {
+      const int id = c.id(a), left = c.item_left(a);
+      c.pos += w - c.real;
+      u += w;
+      if (u < n) {
         c.settle(a);
         if (c.id(a) == id) continue;
+      }
+      if (first) {  // the end of another pair's item: no block of it was here
+        if (u < n) seg_pos = c.item_pos(a);
+        continue;
       }
       // ---- the item's (or this pair's) last block: the partial sums of its rows
       const int pb = (i - 1) % PA_NP;
@@ -673,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       m_used = -INFINITY;
       l = 0.f;
       first = true;
-      if (i < n) seg_pos = c.item_pos(a);
+      if (u < n) seg_pos = c.item_pos(a);
     }
   }
   if (!ok) {
