@@ -112,7 +112,8 @@ def test_norm_rope_strides_and_in_place():
     wide = _randn(g, T, H, 640).bfloat16()
     heads_first = _randn(g, H, T, D).bfloat16().transpose(0, 1)
     one = _randn(g, T, 1, D).bfloat16().expand(T, H, D)
-    for x in (wide[:, :, 512:576], heads_first, one):
+    every = _randn(g, 1, H, D).bfloat16().expand(T, H, D)
+    for x in (wide[:, :, 512:576], heads_first, one, every):
         y = torch.empty(T, H, D, dtype=torch.bfloat16, device=DEV)
         lsa.lsa_norm_rope(x, y, pos, freqs, norm="rms")
         check_rows(y, rotate64(norm64(x, "rms", None, None, 1e-6), pos, freqs, 0, "interleaved", mul))
@@ -213,6 +214,35 @@ def test_cache_append_plain_copy_and_strides():
     assert torch.equal(kv[slot], a) and torch.equal(kc[slot], k) and not kv[:9].any() and not kc[:9].any()
 
 
+def test_cache_append_codes_as_float8_and_unaligned_weights():
+    """A cache of the codes' own type; weights that begin four bytes off a 16-byte boundary."""
+    g, n = _gen(8), 12
+    a, k = _randn(g, 3, 576).bfloat16(), _randn(g, 3, 128).bfloat16()
+    wa, wk = (1 + 0.2 * _randn(g, 513))[1:], (1 + 0.2 * _randn(g, 129))[1:]
+    kv = torch.zeros(n, 576, dtype=torch.bfloat16, device=DEV)
+    kc, ks = torch.zeros(n, 128, device=DEV).to(torch.float8_e4m3fn), torch.zeros(n, device=DEV)
+    slot = torch.tensor([11, 0, 5], device=DEV)
+    lsa.lsa_cache_append(a, kv, slot, kv_weight=wa, k=k, k_cache=kc, k_scale=ks, k_norm="rms", k_weight=wk)
+    check_rows(kv[slot][:, :512], norm64(a[:, :512], "rms", wa, None, 1e-6))
+    check_codes(kc.view(torch.uint8)[slot], ks[slot], norm64(k, "rms", wk, None, 1e-6))
+
+
+def test_cache_append_refusals():
+    a, kv = torch.zeros(3, 576, dtype=torch.bfloat16, device=DEV), torch.zeros(8, 576, dtype=torch.bfloat16, device=DEV)
+    k, kc, ks = a[:, :128].contiguous(), kv[:, :128].contiguous(), torch.zeros(8, device=DEV)
+    slot, pos, freqs = torch.arange(3, device=DEV), torch.arange(3, device=DEV), lsa.lsa_rope_freqs(64)[0]
+    for args, kw in (((a, kv, slot.int()), {}), ((a[:2], kv, slot), {}), ((a.float(), kv, slot), {}), ((a, kv.t(), slot), {}),
+                     ((a, kv, slot), dict(pos=pos)), ((a, kv, slot), dict(freqs=freqs)),
+                     ((a, kv, slot), dict(pos=pos, freqs=lsa.lsa_rope_freqs(32)[0])), ((a, kv, slot), dict(k=k)),
+                     ((a, kv, slot), dict(k=k, k_cache=kc[:4])), ((a, kv, slot), dict(k=k, k_cache=kc, k_scale=ks)),
+                     ((a, kv, slot), dict(k=k, k_cache=kc, k_norm="layer", k_weight=torch.ones(64, device=DEV))),
+                     ((a, kv, slot), dict(k=k, k_cache=kc, k_rope_off=0)),
+                     ((a, kv, slot), dict(kv_weight=torch.ones(576, device=DEV)))):
+        with pytest.raises(lsa.LsaError):
+            lsa.lsa_cache_append(*args, **kw)
+    assert not kv.any() and not kc.any()
+
+
 def test_cache_append_slots_outside_are_skipped_and_reported():
     g, n = _gen(6), 20
     a, kv = _randn(g, 5, 576).bfloat16(), _randn(g, n, 576).bfloat16()
@@ -281,6 +311,54 @@ def test_prefix_attn(B, H, Lp, lens, page):
     q, prefix, pages, table, own = _prefix_case(B * 31 + H, B, H, Lp, lens, page)
     out, lse = _run_prefix(q, prefix, pages, table, own, 576 ** -0.5)
     check_prefix(out, lse, q, prefix, 576 ** -0.5, pages, table, own, rows=range(0, B, 1 if B <= 40 else 7))
+    _status_ok()
+
+
+@pytest.mark.parametrize("B,H,Lp,lens,page", [
+    (400, 128, 130, [b % 3 for b in range(400)], 16),          # more tiles than threads that count them
+    (300, 33, 70, [(7 * b) % 40 for b in range(300)], 8),      # many tiles of several queries
+    (150, 48, 0, [(29 * b) % 300 for b in range(150)], 128),   # own tokens alone, items over several pairs
+    (6, 64, 3000, [1500, 0, 0, 700, 1, 129], 64), (2, 130, 777, [260, 3], 16), (80, 128, 127, None, 0)])
+def test_prefix_attn_many_tiles(B, H, Lp, lens, page):
+    q, prefix, pages, table, own = _prefix_case(B + H, B, H, Lp, lens, page)
+    out, lse = _run_prefix(q, prefix, pages, table, own, 0.04)
+    check_prefix(out, lse, q, prefix, 0.04, pages, table, own, rows=sorted({0, 1, B // 3, B // 2, B - 2, B - 1} & set(range(B))))
+    assert torch.isfinite(out.float()).all() or lens is not None
+    again, lse2 = _run_prefix(q, prefix, pages, table, own, 0.04)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    _status_ok()
+
+
+def test_prefix_attn_past_32_bit_offsets():
+    """A prefix of more than 2^32 bytes and 2^31 elements: rows of zeros (logit 0, value 0) but for the last 300."""
+    g, B, H, L, n = _gen(51), 2, 16, (1 << 31) // 576 + 1001, 300
+    prefix = torch.zeros(L, 576, dtype=torch.bfloat16, device=DEV)
+    prefix[-n:] = _randn(g, n, 576).bfloat16()
+    q = (8 * _randn(g, B, H, 576)).bfloat16()
+    out, lse = _run_prefix(q, prefix, None, None, None, 0.04)
+    k = prefix[-n:].double()
+    z = 0.04 * q.double() @ k.T
+    l = torch.logaddexp(torch.logsumexp(z, -1), torch.full((B, H), math.log(L - n), dtype=torch.float64, device=DEV))
+    p = torch.exp(z - l[..., None])
+    o, mag = p @ k[:, :512], p @ k[:, :512].abs()
+    dz = 0.04 * float((q.double().abs() @ k.abs().T).max()) * 576 * 2.0 ** -23
+    assert ((out.double() - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.1 * dz + 2.0 ** -12) * mag * (1 + 2.0 ** -8)).all()
+    # 32-bit sums of 2^22 equal terms, four at a time and then joined: 2^-18 of the sum
+    assert ((lse.double() - l).abs() <= dz + 2.0 ** -16 * (1 + l.abs())).all()
+    assert out.any()
+
+
+def test_prefix_attn_empty_tables_and_slices():
+    """A table without columns, a cache without pages, an empty prefix, a prefix that is a slice of a longer cache."""
+    q, cache, pages, table, own = _prefix_case(50, 3, 16, 500, [0, 0, 0], 16)
+    prefix = cache[100:357]
+    want = _run_prefix(q, prefix, None, None, None, 0.04)
+    check_prefix(*want, q, prefix, 0.04)
+    for pg, tb in ((pages, table[:, :0].contiguous()), (pages[:0], table)):
+        got = _run_prefix(q, prefix, pg, tb, own, 0.04)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    out, lse = _run_prefix(q, cache[:0], pages, table, own, 0.04)
+    assert not out.any() and bool((lse == -math.inf).all())
     _status_ok()
 
 
