@@ -147,8 +147,9 @@ struct NormRopeArgs {
 // instruction.  Small blocks (128 threads, six an SM) wait for each other least: 43.4 us against 44.6 at 256 threads and
 // 70 at 512; a grid of resident blocks with two tables in turn took 55.
 // 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 45.6 us, 5890 GB/s.  2047 x 128 rows of 64, no norm, into
-// their place in rows of 1152 bytes: 17.9 us cold, 3750 GB/s (128-byte pieces of HBM pages; 11 us in the L2).  4099 x 64 rows of 128, layer norm, to codes: 29.4 us, 3460 GB/s, bound by its instructions (three reductions
-// and a scale a row, 17 operations an element).
+// their place in rows of 1152 bytes: 17.4 us cold, 3850 GB/s (128-byte pieces of HBM pages; 11 us in the L2).
+// 4099 x 64 rows of 128, layer norm, to codes: 29.6 us, 3440 GB/s, bound by its instructions (21 an element: three
+// reductions and a scale a row; 60% of the issue slots at 24 warps an SM, and neither more warps nor larger blocks help).
 template <int G, int ITER, int NORM, bool FP8>
 __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(const NormRopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin | weight [D] | bias [D]
