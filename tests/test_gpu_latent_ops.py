@@ -541,6 +541,42 @@ def test_streams_graphs_and_repeats():
     _status_ok()
 
 
+def test_explicit_stream_and_another_current_device(monkeypatch):
+    """A stream given to the call; and a current device that is not the tensors' (as far as one GPU can show it: the calls
+    make the tensors' device current and give the same)."""
+    q, prefix, pages, table, own = _prefix_case(60, 3, 32, 400, [20, 0, 50], 16)
+    want = _run_prefix(q, prefix, pages, table, own, 0.04)
+    freqs, _ = lsa.lsa_rope_freqs(64)
+    pos = torch.arange(3, device=DEV)
+    a = q[:, 0].contiguous()
+
+    def run(**kw):
+        out, lse = torch.empty(3, 32, 512, dtype=torch.bfloat16, device=DEV), torch.empty(3, 32, device=DEV)
+        ws = lsa.workspace(lsa.lsa_prefix_attn_workspace_size(3, 32), DEV)
+        y, kv = torch.empty_like(q), torch.zeros(4, 576, dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        lsa.lsa_norm_rope(q, y, pos, freqs, rope_off=512, **kw)
+        lsa.lsa_cache_append(a, kv, pos, pos, freqs, **kw)
+        lsa.lsa_prefix_attn(q, prefix, 0.04, out, lse, pages=pages, table=table, own_len=own, ws=ws, **kw)
+        torch.cuda.synchronize()
+        return out, lse, y, kv
+
+    plain, side = run(), run(stream=torch.cuda.Stream())
+    answers = []
+
+    def first_yes(t):  # another device is current, until the call has made the tensors' own the current one
+        answers.append(len(answers) % 2 == 0)
+        return answers[-1]
+
+    monkeypatch.setattr(lsa, "_off_device", first_yes)
+    moved = run()
+    monkeypatch.undo()
+    assert len(answers) == 6  # each call asked twice
+    for got in (plain, side, moved):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(got[2], plain[2]) and torch.equal(got[3], plain[3])
+
+
 def test_decode_steps_together():
     """A few decode steps of a layer as a server runs them: queries normed and rotated, rows appended to pages, the index
     scored over them and its top-K attended to, and dense attention over prefix and own pages; against 64 bits."""
