@@ -667,7 +667,7 @@ int lsa_norm_rope(const void* x, int64_t x_ldt, int64_t x_ldh, int64_t T, int H,
   LSA_CHECK_ARG(norm == LSA_NORM_NONE || (eps >= 0.f && eps < 1e30f));
   LSA_CHECK_ARG(dtype == LSA_BF16 || dtype == LSA_FP8_E4M3);
   LSA_CHECK_ARG((dtype == LSA_FP8_E4M3) == (y_scale != nullptr));
-  if (D % 8 != 0 || D > 1024) return LSA_ERR_UNSUPPORTED;
+  if (D % 8 != 0 || D > 1024 || T > (int64_t(1) << 40)) return LSA_ERR_UNSUPPORTED;
   if (freqs) {
     LSA_CHECK_ARG(layout == LSA_ROPE_INTERLEAVED || layout == LSA_ROPE_HALF);
     LSA_CHECK_ARG(rope_off >= 0 && rope_dims >= 2 && rope_off <= D - rope_dims);
@@ -687,7 +687,7 @@ int lsa_cache_append(const void* a, int64_t a_ld, int64_t T, int d_qk, int d_v, 
                      const float* k_bias, float k_eps, int k_rope_off, int k_layout, void* k_cache, int k_dtype,
                      float* k_scale, void* stream) {
   LSA_CHECK_ARG(T >= 0 && n_slots >= 0);
-  if (d_qk != 576 || d_v != 512) return LSA_ERR_UNSUPPORTED;
+  if (d_qk != 576 || d_v != 512 || T > (int64_t(1) << 40)) return LSA_ERR_UNSUPPORTED;
   LSA_CHECK_ARG(kv_weight == nullptr || (kv_eps >= 0.f && kv_eps < 1e30f));
   LSA_CHECK_ARG(freqs == nullptr || layout == LSA_ROPE_INTERLEAVED || layout == LSA_ROPE_HALF);
   if (k) {
@@ -724,7 +724,7 @@ int lsa_prefix_attn(const void* q, int64_t B, int H, int d_qk, int d_v, const vo
                     const void* pages, int64_t n_pages, int page, const int32_t* table, int64_t table_ld,
                     const int32_t* own_len, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
                     void* stream) {
-  LSA_CHECK_ARG(B >= 0 && H >= 1 && H <= 65535 && Lp >= 0 && n_pages >= 0 && table_ld >= 0);
+  LSA_CHECK_ARG(B >= 0 && B <= 65535 && H >= 1 && H <= 65535 && Lp >= 0 && n_pages >= 0 && table_ld >= 0);
   LSA_CHECK_ARG(scale > -1e30f && scale < 1e30f);
   if (d_qk != 576 || d_v != 512) return LSA_ERR_UNSUPPORTED;
   if (own_len) {
@@ -736,7 +736,6 @@ int lsa_prefix_attn(const void* q, int64_t B, int H, int d_qk, int d_v, const vo
   }
   if (Lp > 0x7FFF0000 || B * H > 0x7FFF0000) return LSA_ERR_UNSUPPORTED;
   if (B == 0) return LSA_OK;
-  LSA_CHECK_ARG(B <= 65535);
   LSA_CHECK_ARG(q && out && (Lp == 0 || prefix));
   LSA_CHECK_ARG(aligned16(q) && aligned16(out) && (Lp == 0 || aligned16(prefix)));
   if (own_len) {

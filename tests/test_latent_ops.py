@@ -53,7 +53,7 @@ def _norm_rope(lib, **kw):
     (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(H=65536), INVALID), (dict(D=0), INVALID), (dict(norm=3), INVALID),
     (dict(norm=0), INVALID), (dict(bias=FAKE), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=math.nan), INVALID),
     (dict(dtype=2), INVALID), (dict(dtype=1), INVALID), (dict(y_scale=FAKE), INVALID), (dict(D=100), UNSUPPORTED),
-    (dict(D=1032), UNSUPPORTED), (dict(layout=2), INVALID), (dict(off=-8), INVALID), (dict(off=72), INVALID),
+    (dict(D=1032), UNSUPPORTED), (dict(T=1 << 62), UNSUPPORTED), (dict(layout=2), INVALID), (dict(off=-8), INVALID), (dict(off=72), INVALID),
     (dict(off=4), UNSUPPORTED), (dict(R=24), UNSUPPORTED), (dict(R=0), INVALID), (dict(R=136), INVALID),
     (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(pos=None), INVALID), (dict(x=FAKE + 8), INVALID),
     (dict(y=FAKE + 8), INVALID), (dict(x_ldt=8191), INVALID), (dict(y_ldh=132), INVALID), (dict(T=0, x=None), 0)])
@@ -96,7 +96,7 @@ def _prefix(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(B=-1), INVALID), (dict(B=65536), INVALID), (dict(H=0), INVALID), (dict(H=65536), INVALID), (dict(Lp=-1), INVALID),
+    (dict(B=-1), INVALID), (dict(B=65536), INVALID), (dict(B=1 << 62), INVALID), (dict(H=0), INVALID), (dict(H=65536), INVALID), (dict(Lp=-1), INVALID),
     (dict(n_pages=-1), INVALID), (dict(table_ld=-1), INVALID), (dict(scale=math.nan), INVALID),
     (dict(scale=math.inf), INVALID), (dict(d_qk=512), UNSUPPORTED), (dict(d_v=576), UNSUPPORTED), (dict(page=0), INVALID),
     (dict(page=4), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(page=1 << 17), UNSUPPORTED),
