@@ -512,6 +512,73 @@ int lsa_prefix_attn(const void* q, int64_t B, int H, int d_qk, int d_v, const vo
                     const int32_t* own_len, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
                     void* stream);
 
+/*
+ * lsa_norm_rope_packed, lsa_cache_append_packed, lsa_prefix_attn_packed -- the three calls above with their arguments in a
+ *   struct, for callers to whom each argument of a call costs (a binding that converts them one by one: 2.8 us for
+ *   lsa_norm_rope's 22, 0.6 us for the struct).  size: sizeof of the struct, else LSA_ERR_INVALID_ARG.  The fields are the
+ *   arguments of the same names; the struct is read before the call returns and need not be aligned.
+ */
+typedef struct {
+  uint64_t size;
+  const void* x;
+  int64_t x_ldt, x_ldh, T;
+  const float* weight;
+  const float* bias;
+  const double* freqs;
+  const int64_t* pos;
+  void* y;
+  int64_t y_ldt, y_ldh;
+  float* y_scale;
+  void* stream;
+  int32_t H, D, norm, rope_off, rope_dims, layout, dtype;
+  float eps, mul;
+} lsa_norm_rope_args;
+
+typedef struct {
+  uint64_t size;
+  const void* a;
+  int64_t a_ld, T;
+  const float* kv_weight;
+  const double* freqs;
+  const int64_t* pos;
+  const int64_t* slot;
+  void* kv;
+  int64_t n_slots;
+  const void* k;
+  int64_t k_ld;
+  const float* k_weight;
+  const float* k_bias;
+  void* k_cache;
+  float* k_scale;
+  void* stream;
+  int32_t d_qk, d_v, layout, d_I, k_norm, k_rope_off, k_layout, k_dtype;
+  float kv_eps, mul, k_eps;
+} lsa_cache_append_args;
+
+typedef struct {
+  uint64_t size;
+  const void* q;
+  int64_t B;
+  const void* prefix;
+  int64_t Lp;
+  const void* pages;
+  int64_t n_pages;
+  const int32_t* table;
+  int64_t table_ld;
+  const int32_t* own_len;
+  void* out;
+  float* lse;
+  void* ws;
+  uint64_t ws_bytes;
+  void* stream;
+  int32_t H, d_qk, d_v, page;
+  float scale;
+} lsa_prefix_attn_args;
+
+int lsa_norm_rope_packed(const void* args);
+int lsa_cache_append_packed(const void* args);
+int lsa_prefix_attn_packed(const void* args);
+
 /* lsa_prefix_attn_workspace_size -- scratch bytes of lsa_prefix_attn; (size_t)-1 for invalid sizes. */
 size_t lsa_prefix_attn_workspace_size(int64_t B, int H);
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -69,6 +70,9 @@ SIGNATURES = {
     "lsa_prefix_attn": (_I32, [_P, _I64, _I32, _I32, _I32, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _F32, _P, _P, _P,
                                _SZ, _P]),
     "lsa_prefix_attn_workspace_size": (_SZ, [_I64, _I32]),
+    "lsa_norm_rope_packed": (_I32, [ctypes.c_char_p]),
+    "lsa_cache_append_packed": (_I32, [ctypes.c_char_p]),
+    "lsa_prefix_attn_packed": (_I32, [ctypes.c_char_p]),
     "lsa_workspace_size": (_SZ, [_I32, _I64, _I64, _I32, _I32, _I32, _I32]),
     "lsa_device_status": (_I32, [_P]),
     "lsa_selftest_wait": (_I32, [ctypes.c_uint64, _P]),
@@ -311,8 +315,13 @@ def lsa_msa_attn(q, kv, idx, gmask, count, G, scale, out, lse=None, ws=None, str
     _check("lsa_msa_attn", st)
 
 
-# The calls below take a few microseconds on the GPU in a decode step, so their checks are written to cost little: one test
-# a tensor, messages formed on failure only, the stream asked for as a number (a Stream object costs 3 us).
+# The calls below take a few microseconds on the GPU in a decode step, so they are written to cost little: one test a
+# tensor, messages formed on failure only, the stream asked for as a number (a Stream object costs 3 us), the arguments
+# packed into the C struct of the *_packed forms (22 converted arguments cost 2.8 us, the struct 0.6).
+# (0Q: a C struct is padded to its widest field.)
+_NORM_ROPE = struct.Struct("@QQqqqQQQQQqqQQ7i2f0Q")
+_CACHE_APPEND = struct.Struct("@QQqqQQQQQqQqQQQQQ8i3f0Q")
+_PREFIX_ATTN = struct.Struct("@QQqQqQqQqQQQQQQ4if0Q")
 
 
 def _bad(fn: str, what: str):
@@ -331,10 +340,10 @@ def _ten(fn: str, name: str, t, dtype, shape, dev: int):
 
 
 def _vec(fn: str, name: str, t, dtype, n: int, dev: int):
-    """Address of an optional contiguous vector of n elements."""
+    """Address of n contiguous elements, or 0 for None."""
     if t is None:
-        return None
-    if t.dtype is dtype and t.numel() == n and t.dim() == 1 and t.get_device() == dev and t.is_contiguous():
+        return 0
+    if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     _refuse(fn, name, t, dtype, (n,), dev)
 
@@ -346,13 +355,13 @@ def _code(fn: str, name: str, table: dict, key) -> int:
     return c
 
 
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _off_device(t) -> bool:
+def _off_device(dev: int) -> bool:
     """Whether the call has to make the tensors' GPU the current one first."""
-    return t.get_device() != torch._C._cuda_getDevice()
+    return dev != _get_device()
 
 
 def lsa_rope_freqs(R, base=10000.0, scaling="none", factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0,
@@ -373,11 +382,11 @@ def lsa_norm_rope(x, y, pos=None, freqs=None, norm="none", weight=None, bias=Non
     fn = "lsa_norm_rope"
     if x.dim() != 3 or not x.is_cuda or x.dtype is not _bf16:
         _bad(fn, "x: bf16 [T, H, D] on a GPU wanted")
-    if _off_device(x):
+    dev = x.get_device()
+    if _off_device(dev):
         with torch.cuda.device(x.device):
             return lsa_norm_rope(x, y, pos, freqs, norm, weight, bias, eps, rope_off, layout, mul, y_scale, stream)
     T, H, D = shape = x.shape
-    dev = x.get_device()
     if y.shape != shape or y.get_device() != dev:
         _bad(fn, "y: the shape and device of x wanted")
     (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
@@ -398,12 +407,13 @@ def lsa_norm_rope(x, y, pos=None, freqs=None, norm="none", weight=None, bias=Non
         R = 2 * freqs.shape[0]
     elif pos is not None:
         _bad(fn, "pos without freqs")
-    st = (_lib or load_library()).lsa_norm_rope(
-        x.data_ptr(), xt, xh, T, H, D, _code(fn, "norm", _NORMS, norm), _vec(fn, "weight", weight, _f32, D, dev),
-        _vec(fn, "bias", bias, _f32, D, dev), eps, _vec(fn, "freqs", freqs, _f64, R // 2, dev), rope_off, R,
-        _code(fn, "layout", _LAYOUTS, layout), mul, _vec(fn, "pos", pos, _i64, T, dev), y.data_ptr(), yt, yh,
-        _dtype_code(y), None if y_scale is None else _ten(fn, "y_scale", y_scale, _f32, (T, H), dev),
-        _raw_stream(stream, dev))
+    st = (_lib or load_library()).lsa_norm_rope_packed(_NORM_ROPE.pack(
+        _NORM_ROPE.size, x.data_ptr(), xt, xh, T, _vec(fn, "weight", weight, _f32, D, dev),
+        _vec(fn, "bias", bias, _f32, D, dev), _vec(fn, "freqs", freqs, _f64, R // 2, dev),
+        _vec(fn, "pos", pos, _i64, T, dev), y.data_ptr(), yt, yh,
+        0 if y_scale is None else _ten(fn, "y_scale", y_scale, _f32, (T, H), dev),
+        _get_stream(dev) if stream is None else stream.cuda_stream, H, D, _code(fn, "norm", _NORMS, norm), rope_off, R,
+        _code(fn, "layout", _LAYOUTS, layout), _dtype_code(y), eps, mul))
     if st:
         _check(fn, st)
 
@@ -425,15 +435,16 @@ def lsa_cache_append(a, kv, slot, pos=None, freqs=None, kv_weight=None, kv_eps=1
     fn = "lsa_cache_append"
     if not a.is_cuda or slot.dim() != 1 or kv.dim() != 2:
         _bad(fn, "a [T, 576], kv [slots, 576] and slot [T] on a GPU wanted")
-    if _off_device(a):
+    dev = a.get_device()
+    if _off_device(dev):
         with torch.cuda.device(a.device):
             return lsa_cache_append(a, kv, slot, pos, freqs, kv_weight, kv_eps, layout, mul, k, k_cache, k_scale, k_norm,
                                     k_weight, k_bias, k_eps, k_rope_off, k_layout, stream)
-    dev, T, n = a.get_device(), slot.shape[0], kv.shape[0]
+    T, n = slot.shape[0], kv.shape[0]
     if (freqs is None) != (pos is None) or (k is None) != (k_cache is None):
         _bad(fn, "freqs and pos, and k and k_cache, belong together")
     a_ld = _rows(fn, "a", a, T, 576, dev)
-    k_p, k_ld, d_I, k_dtype, kc_p = None, 0, 0, 0, None
+    k_p = k_ld = d_I = k_dtype = kc_p = 0
     if k is not None:
         if k.dim() != 2:
             _bad(fn, "k [T, d_I] wanted")
@@ -442,13 +453,14 @@ def lsa_cache_append(a, kv, slot, pos=None, freqs=None, kv_weight=None, kv_eps=1
         kc_p = _ten(fn, "k_cache", k_cache, k_cache.dtype, (n, d_I), dev)
     else:
         k_rope_off = -1
-    st = (_lib or load_library()).lsa_cache_append(
-        a.data_ptr(), a_ld, T, 576, 512, _vec(fn, "kv_weight", kv_weight, _f32, 512, dev), kv_eps,
-        _vec(fn, "freqs", freqs, _f64, 32, dev), _code(fn, "layout", _LAYOUTS, layout), mul,
-        _vec(fn, "pos", pos, _i64, T, dev), _vec(fn, "slot", slot, _i64, T, dev), _ten(fn, "kv", kv, _bf16, (n, 576), dev), n,
-        k_p, k_ld, d_I, _code(fn, "k_norm", _NORMS, k_norm), _vec(fn, "k_weight", k_weight, _f32, d_I, dev),
-        _vec(fn, "k_bias", k_bias, _f32, d_I, dev), k_eps, k_rope_off, _code(fn, "k_layout", _LAYOUTS, k_layout), kc_p,
-        k_dtype, _vec(fn, "k_scale", k_scale, _f32, n, dev), _raw_stream(stream, dev))
+    st = (_lib or load_library()).lsa_cache_append_packed(_CACHE_APPEND.pack(
+        _CACHE_APPEND.size, a.data_ptr(), a_ld, T, _vec(fn, "kv_weight", kv_weight, _f32, 512, dev),
+        _vec(fn, "freqs", freqs, _f64, 32, dev), _vec(fn, "pos", pos, _i64, T, dev), _vec(fn, "slot", slot, _i64, T, dev),
+        _ten(fn, "kv", kv, _bf16, (n, 576), dev), n, k_p, k_ld, _vec(fn, "k_weight", k_weight, _f32, d_I, dev),
+        _vec(fn, "k_bias", k_bias, _f32, d_I, dev), kc_p, _vec(fn, "k_scale", k_scale, _f32, n, dev),
+        _get_stream(dev) if stream is None else stream.cuda_stream, 576, 512, _code(fn, "layout", _LAYOUTS, layout), d_I,
+        _code(fn, "k_norm", _NORMS, k_norm), k_rope_off, _code(fn, "k_layout", _LAYOUTS, k_layout), k_dtype, kv_eps, mul,
+        k_eps))
     if st:
         _check(fn, st)
 
@@ -463,17 +475,17 @@ def lsa_prefix_attn(q, prefix, scale, out, lse=None, pages=None, table=None, own
     fn = "lsa_prefix_attn"
     if q.dim() != 3 or not q.is_cuda or out.dim() != 3:
         _bad(fn, "q [B, H, 576] and out [B, H, 512] on a GPU wanted")
-    if _off_device(q):
+    dev = q.get_device()
+    if _off_device(dev):
         with torch.cuda.device(q.device):
             return lsa_prefix_attn(q, prefix, scale, out, lse, pages, table, own_len, ws, stream)
-    dev = q.get_device()
     B, H, d_qk = q_shape = q.shape
-    d_v, Lp, prefix_p = out.shape[2], 0, None
+    d_v, Lp, prefix_p = out.shape[2], 0, 0
     if prefix is not None:
         Lp = prefix.shape[0]
         prefix_p = _ten(fn, "prefix", prefix, _bf16, (Lp, d_qk), dev)
     n_pages = page = cols = 0
-    pages_p = table_p = None
+    pages_p = table_p = 0
     if own_len is not None:
         if pages is None or table is None or pages.dim() != 3 or table.dim() != 2:
             _bad(fn, "pages [n_pages, page, 576] and table [B, cols] wanted with own_len")
@@ -487,10 +499,11 @@ def lsa_prefix_attn(q, prefix, scale, out, lse=None, pages=None, table=None, own
         if ws.get_device() != dev or not ws.is_contiguous():
             _bad(fn, "ws: contiguous bytes on the GPU of q wanted")
         ws_p, ws_n = ws.data_ptr(), ws.numel() * ws.element_size()
-    st = (_lib or load_library()).lsa_prefix_attn(
-        _ten(fn, "q", q, _bf16, q_shape, dev), B, H, d_qk, d_v, prefix_p, Lp, pages_p, n_pages, page, table_p, cols,
-        _vec(fn, "own_len", own_len, _i32, B, dev), scale, _ten(fn, "out", out, _bf16, (B, H, d_v), dev),
-        None if lse is None else _ten(fn, "lse", lse, _f32, (B, H), dev), ws_p, ws_n, _raw_stream(stream, dev))
+    st = (_lib or load_library()).lsa_prefix_attn_packed(_PREFIX_ATTN.pack(
+        _PREFIX_ATTN.size, _ten(fn, "q", q, _bf16, q_shape, dev), B, prefix_p, Lp, pages_p, n_pages, table_p, cols,
+        _vec(fn, "own_len", own_len, _i32, B, dev), _ten(fn, "out", out, _bf16, (B, H, d_v), dev),
+        0 if lse is None else _ten(fn, "lse", lse, _f32, (B, H), dev), ws_p, ws_n,
+        _get_stream(dev) if stream is None else stream.cuda_stream, H, d_qk, d_v, page, scale))
     if st:
         _check(fn, st)
 

@@ -748,3 +748,42 @@ int lsa_prefix_attn(const void* q, int64_t B, int H, int d_qk, int d_v, const vo
 }
 
 }  // extern "C"
+
+namespace lsa {
+// the struct of a packed call, whose size comes first
+template <typename T>
+static bool unpack(const void* p, T* a) {
+  uint64_t size = 0;
+  if (p == nullptr) return false;
+  std::memcpy(&size, p, sizeof(size));
+  if (size != sizeof(T)) return false;
+  std::memcpy(a, p, sizeof(T));
+  return true;
+}
+}  // namespace lsa
+
+extern "C" {
+
+int lsa_norm_rope_packed(const void* args) {
+  lsa_norm_rope_args a;
+  LSA_CHECK_ARG(unpack(args, &a));
+  return lsa_norm_rope(a.x, a.x_ldt, a.x_ldh, a.T, a.H, a.D, a.norm, a.weight, a.bias, a.eps, a.freqs, a.rope_off,
+                       a.rope_dims, a.layout, a.mul, a.pos, a.y, a.y_ldt, a.y_ldh, a.dtype, a.y_scale, a.stream);
+}
+
+int lsa_cache_append_packed(const void* args) {
+  lsa_cache_append_args a;
+  LSA_CHECK_ARG(unpack(args, &a));
+  return lsa_cache_append(a.a, a.a_ld, a.T, a.d_qk, a.d_v, a.kv_weight, a.kv_eps, a.freqs, a.layout, a.mul, a.pos, a.slot,
+                          a.kv, a.n_slots, a.k, a.k_ld, a.d_I, a.k_norm, a.k_weight, a.k_bias, a.k_eps, a.k_rope_off,
+                          a.k_layout, a.k_cache, a.k_dtype, a.k_scale, a.stream);
+}
+
+int lsa_prefix_attn_packed(const void* args) {
+  lsa_prefix_attn_args a;
+  LSA_CHECK_ARG(unpack(args, &a));
+  return lsa_prefix_attn(a.q, a.B, a.H, a.d_qk, a.d_v, a.prefix, a.Lp, a.pages, a.n_pages, a.page, a.table, a.table_ld,
+                         a.own_len, a.scale, a.out, a.lse, a.ws, static_cast<size_t>(a.ws_bytes), a.stream);
+}
+
+}  // extern "C"

@@ -564,7 +564,7 @@ def test_explicit_stream_and_another_current_device(monkeypatch):
     plain, side = run(), run(stream=torch.cuda.Stream())
     answers = []
 
-    def first_yes(t):  # another device is current, until the call has made the tensors' own the current one
+    def first_yes(dev):  # another device is current, until the call has made the tensors' own the current one
         answers.append(len(answers) % 2 == 0)
         return answers[-1]
 

@@ -118,6 +118,48 @@ def test_prefix_attn_workspace_size(lib):
         assert lib.lsa_prefix_attn_workspace_size(B, H) == bad
 
 
+def test_packed_forms(lib):
+    """The structs that the binding packs are the library's: their sizes are taken, every field lands where the plain call
+    has it (each refusal of one field), and another size is refused."""
+    z = dict(size=lsa._NORM_ROPE.size, x=FAKE, x_ldt=64, x_ldh=64, T=0, weight=0, bias=0, freqs=0, pos=0, y=FAKE, y_ldt=64,
+             y_ldh=64, y_scale=0, stream=0, H=1, D=64, norm=0, rope_off=0, rope_dims=0, layout=0, dtype=0, eps=1.0, mul=1.0)
+    call = lambda **kw: lib.lsa_norm_rope_packed(lsa._NORM_ROPE.pack(*dict(z, **kw).values()))
+    assert call() == 0 and call(size=8) == INVALID and lib.lsa_norm_rope_packed(None) == INVALID
+    for kw, want in ((dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(D=12), UNSUPPORTED), (dict(norm=5), INVALID),
+                     (dict(weight=FAKE), INVALID), (dict(bias=FAKE), INVALID), (dict(norm=1, eps=-1.0), INVALID),
+                     (dict(dtype=1), INVALID), (dict(y_scale=FAKE), INVALID), (dict(freqs=FAKE), INVALID),
+                     (dict(freqs=FAKE, rope_dims=16, rope_off=4), UNSUPPORTED), (dict(freqs=FAKE, rope_dims=16, layout=2), INVALID),
+                     (dict(T=1, x=0), INVALID), (dict(T=1, y=0), INVALID), (dict(T=1, x_ldt=1), INVALID),
+                     (dict(T=1, x_ldh=1), INVALID), (dict(T=1, y_ldt=1), INVALID), (dict(T=1, y_ldh=1), INVALID),
+                     (dict(T=1, freqs=FAKE, rope_dims=16), INVALID)):
+        assert call(**kw) == want, kw
+    z = dict(size=lsa._CACHE_APPEND.size, a=FAKE, a_ld=576, T=0, kv_weight=0, freqs=0, pos=0, slot=FAKE, kv=FAKE, n_slots=4,
+             k=0, k_ld=0, k_weight=0, k_bias=0, k_cache=0, k_scale=0, stream=0, d_qk=576, d_v=512, layout=0, d_I=0, k_norm=0,
+             k_rope_off=-1, k_layout=0, k_dtype=0, kv_eps=0.0, mul=1.0, k_eps=0.0)
+    call = lambda **kw: lib.lsa_cache_append_packed(lsa._CACHE_APPEND.pack(*dict(z, **kw).values()))
+    keys = dict(k=FAKE, k_ld=128, d_I=128, k_cache=FAKE)
+    assert call() == 0 and call(**keys) == 0 and call(size=0) == INVALID and lib.lsa_cache_append_packed(None) == INVALID
+    for kw, want in ((dict(T=-1), INVALID), (dict(n_slots=-1), INVALID), (dict(d_qk=1), UNSUPPORTED), (dict(d_v=1), UNSUPPORTED),
+                     (dict(kv_weight=FAKE, kv_eps=-1.0), INVALID), (dict(freqs=FAKE, layout=3), INVALID),
+                     (dict(k_cache=FAKE), INVALID), (dict(k_scale=FAKE), INVALID), (dict(k_weight=FAKE), INVALID),
+                     (dict(k_bias=FAKE), INVALID), (dict(keys, d_I=7), UNSUPPORTED), (dict(keys, k_norm=9), INVALID),
+                     (dict(keys, k_norm=1, k_eps=-1.0), INVALID), (dict(keys, k_rope_off=0), INVALID),
+                     (dict(keys, k_rope_off=0, freqs=FAKE, k_layout=4), INVALID), (dict(keys, k_dtype=1), INVALID),
+                     (dict(T=1, a=0), INVALID), (dict(T=1, slot=0), INVALID), (dict(T=1, kv=0), INVALID),
+                     (dict(T=1, a_ld=4), INVALID), (dict(keys, T=1, k_ld=4), INVALID), (dict(T=1, freqs=FAKE), INVALID)):
+        assert call(**kw) == want, kw
+    z = dict(size=lsa._PREFIX_ATTN.size, q=FAKE, B=0, prefix=FAKE, Lp=8, pages=FAKE, n_pages=4, table=FAKE, table_ld=2,
+             own_len=FAKE, out=FAKE, lse=0, ws=FAKE, ws_bytes=1 << 40, stream=0, H=8, d_qk=576, d_v=512, page=16, scale=1.0)
+    call = lambda **kw: lib.lsa_prefix_attn_packed(lsa._PREFIX_ATTN.pack(*dict(z, **kw).values()))
+    assert call() == 0 and call(size=1) == INVALID and lib.lsa_prefix_attn_packed(None) == INVALID
+    for kw, want in ((dict(B=-1), INVALID), (dict(H=0), INVALID), (dict(Lp=-1), INVALID), (dict(n_pages=-1), INVALID),
+                     (dict(table_ld=-1), INVALID), (dict(d_qk=1), UNSUPPORTED), (dict(d_v=1), UNSUPPORTED),
+                     (dict(page=3), UNSUPPORTED), (dict(scale=math.nan), INVALID), (dict(B=1, q=0), INVALID),
+                     (dict(B=1, out=0), INVALID), (dict(B=1, prefix=0), INVALID), (dict(B=1, pages=0), INVALID),
+                     (dict(B=1, table=0), INVALID), (dict(B=1, ws=0), WORKSPACE), (dict(B=1, ws_bytes=0), WORKSPACE)):
+        assert call(**kw) == want, kw
+
+
 def _cpu(*shape, dtype=torch.bfloat16):
     return torch.zeros(*shape, dtype=dtype)
 
