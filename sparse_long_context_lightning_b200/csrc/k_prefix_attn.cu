@@ -27,6 +27,8 @@
 // leaves partial sums (fp32) that a second kernel joins, and one that lies in a pair is written at once (74 queries of 128
 // heads with 1000 own tokens each: 30.5 us against 50.3 through partials).  Where a tile holds several queries (H not a multiple of 128),
 // each query's own blocks are an accumulation of their own, so that a row never multiplies another sequence's values.
+#include <algorithm>
+
 #include "lsa_common.cuh"
 #include "sm100_pair.cuh"
 
@@ -818,6 +820,47 @@ __global__ void __launch_bounds__(128) k_prefix_combine_rows(const PaArgs a) {
   if (a.lse && lane == 0) a.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// A warp 128 columns of a row, four columns a lane, a partial's maximum and sum a lane; the first U partials' values are on
+// their way with them.  No shared memory: its blocks can wait on an SM that the attention fills.
+__global__ void __launch_bounds__(128) k_prefix_combine_warps(const PaArgs a) {
+  constexpr int U = 8;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t r64 = blockIdx.x;
+  const int c0 = static_cast<int>(threadIdx.x >> 5) * 128;
+  const uint32_t r = static_cast<uint32_t>(r64);
+  RowParts p;
+  p.find(a, r);
+  if (p.done) return;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int b0 = 0; b0 < p.n; b0 += 32) {
+    const float2 ml = b0 + lane < p.n ? a.ws_ml[p.row(b0 + lane, r)] : make_float2(0.f, 0.f);
+    const int cnt = min(32, p.n - b0);
+    float4 v[U];
+    auto load = [&](int j0) {
+      #pragma unroll
+      for (int k = 0; k < U; ++k)
+        v[k] = j0 + k < cnt ? reinterpret_cast<const float4*>(a.ws_o + p.row(b0 + j0 + k, r) * 512 + c0)[lane]
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    const float mn = fmaxf(m, warp_max(ml.y != 0.f ? ml.x : -INFINITY));
+    const float old = m == -INFINITY ? 0.f : exp2f(m - mn), w = ml.y != 0.f ? exp2f(ml.x - mn) : 0.f;
+    m = mn;
+    l = l * old + warp_sum(w * ml.y);
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+    for (int j0 = 0; j0 < cnt; j0 += U) {
+      #pragma unroll
+      for (int k = 0; k < U; ++k) add_part(acc, __shfl_sync(0xffffffffu, w, (j0 + k) & 31), v[k]);
+      if (j0 + U < cnt) load(j0 + U);
+    }
+  }
+  reinterpret_cast<uint2*>(a.out + r64 * 512 + c0)[lane] = pack4(acc, l != 0.f ? 1.f / l : 0.f);
+  if (a.lse && threadIdx.x == 0) a.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 // Few rows, so many partials each (up to 74): four blocks a row, 128 columns a block; 16 warps take the partials in turn,
 // every load of a row on its way before the weights are formed.  The whole call against one block a row (below): 64 rows
 // of 74 partials 17.8 against 20.2 us, 128 rows of 64 17.4 against 18.1, of 48 17.2 against 16.8, of 8 14.9 against 13.6.
@@ -877,12 +920,11 @@ __global__ void __launch_bounds__(512) k_prefix_combine_few(const PaArgs a) {
 
 // Few rows: a block each.  G groups of 128 threads take the partials in turn (four columns a thread), the weights are
 // formed once a block: a row behind a long prefix has up to 74 partials and few other rows to hide its loads behind.
-template <int G>
-__global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a) {
-  constexpr int U = 6;
-  constexpr int ML = (2 * PA_PAIRS + 128 * G - 1) / (128 * G);  // maxima and sums a thread
+__global__ void __launch_bounds__(512) k_prefix_combine(const PaArgs a) {
+  constexpr int G = 4, U = 6;
+  static_assert(128 * G >= 2 * PA_PAIRS, "a partial's maximum and sum a thread");
   __shared__ float wt[2 * PA_PAIRS];
-  __shared__ float4 acc_s[G > 1 ? (G - 1) * 128 : 1];
+  __shared__ float4 acc_s[(G - 1) * 128];
   __shared__ float red[2 * 4 * G];
   pdl_wait();
   pdl_launch_dependents();
@@ -894,32 +936,21 @@ __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a) {
   auto slot_row = [&](int i) { return p.row(i, r); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = tid & 127;
   // the parts' maxima and sums, and the first of the values on their way at the same time
-  float2 ml[ML];
-  #pragma unroll
-  for (int k = 0; k < ML; ++k)
-    ml[k] = tid + 128 * G * k < parts ? a.ws_ml[slot_row(tid + 128 * G * k)] : make_float2(0.f, 0.f);
+  const float2 ml = tid < parts ? a.ws_ml[slot_row(tid)] : make_float2(0.f, 0.f);
   float4 v[U];
   #pragma unroll
   for (int k = 0; k < U; ++k) {
     const int i = (tid >> 7) + G * k;
     v[k] = i < parts ? reinterpret_cast<const float4*>(a.ws_o + slot_row(i) * 512)[col] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float m = -INFINITY;
-  #pragma unroll
-  for (int k = 0; k < ML; ++k)
-    if (ml[k].y != 0.f) m = fmaxf(m, ml[k].x);
-  m = warp_max(m);
+  float m = warp_max(ml.y != 0.f ? ml.x : -INFINITY);
   if (lane == 0) red[warp] = m;
   __syncthreads();
   #pragma unroll
   for (int w = 0; w < 4 * G; ++w) m = fmaxf(m, red[w]);
-  float l = 0.f;
-  #pragma unroll
-  for (int k = 0; k < ML; ++k) {
-    const float w = ml[k].y != 0.f ? exp2f(ml[k].x - m) : 0.f;
-    if (tid + 128 * G * k < parts) wt[tid + 128 * G * k] = w;
-    l += w * ml[k].y;
-  }
+  const float w_mine = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
+  if (tid < parts) wt[tid] = w_mine;
+  float l = w_mine * ml.y;
   l = warp_sum(l);
   if (lane == 0) red[4 * G + warp] = l;
   __syncthreads();
@@ -941,13 +972,11 @@ __global__ void __launch_bounds__(128 * G) k_prefix_combine(const PaArgs a) {
       v[k] = nx[k];
     }
   }
-  if (G > 1) {
-    if (tid >= 128) acc_s[tid - 128] = acc;
-    __syncthreads();
-    if (tid >= 128) return;
-    #pragma unroll
-    for (int g = 0; g < G - 1; ++g) add_part(acc, 1.f, acc_s[g * 128 + tid]);
-  }
+  if (tid >= 128) acc_s[tid - 128] = acc;
+  __syncthreads();
+  if (tid >= 128) return;
+  #pragma unroll
+  for (int g = 0; g < G - 1; ++g) add_part(acc, 1.f, acc_s[g * 128 + tid]);
   reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(r) * 512)[tid] = pack4(acc, l != 0.f ? 1.f / l : 0.f);
   if (a.lse && tid == 0) a.lse[r] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
@@ -1042,13 +1071,18 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   if (st != LSA_OK) return st;
   LSA_CUDA_TRY(func_smem_once(reinterpret_cast<const void*>(k_prefix_attn), PA_SMEM));
   LSA_CUDA_TRY(launch_pdl(k_prefix_attn, dim3(2 * PA_PAIRS), dim3(PA_THREADS), PA_SMEM, s, 0u, tq, tk, tv, tpk, tpv, a));
-  // a row has about 74 / tiles partials
+  // About how many partials a row has chooses the join.  Few: a warp for 128 columns, against a block a row: 4 tiles of 18
+  // partials 33.5 against 34.6 us, 8 of 9 43.7 against 50.2, one of 8 12.8 against 13.2; 3 tiles of 25 32.5 against 31.3,
+  // one of 12 14.0 against 13.2.  Many tiles, most rows written already: a warp a row (74 tiles 48.8 us against 54.8).
+  const int64_t blocks = a.nP + (own_len && !a.multi ? cdiv(a.cap, PA_T) : 0);  // of a tile, at most
+  const int64_t parts = std::min<int64_t>(blocks, PA_PAIRS / std::min(a.nT, PA_PAIRS)) + (a.multi ? 1 : 0);
   const dim3 rows(static_cast<unsigned>(a.BH));
-  if (a.nT == 1 && a.nP >= 48)
+  if (a.nT > PA_PAIRS / 2)
+    return cuda_status(launch_pdl(k_prefix_combine_rows, dim3(static_cast<unsigned>(cdiv(a.BH, 4))), dim3(128), 0, s, 0u, a));
+  if (a.nT >= 4 || parts <= 8) return cuda_status(launch_pdl(k_prefix_combine_warps, rows, dim3(128), 0, s, 0u, a));
+  if (a.nT == 1 && parts >= 48)
     return cuda_status(launch_pdl(k_prefix_combine_few, dim3(static_cast<unsigned>(4 * a.BH)), dim3(512), 0, s, 0u, a));
-  if (a.nT <= 8) return cuda_status(launch_pdl(k_prefix_combine<4>, rows, dim3(512), 0, s, 0u, a));
-  if (a.nT <= PA_PAIRS / 2) return cuda_status(launch_pdl(k_prefix_combine<1>, rows, dim3(128), 0, s, 0u, a));
-  return cuda_status(launch_pdl(k_prefix_combine_rows, dim3(static_cast<unsigned>(cdiv(a.BH, 4))), dim3(128), 0, s, 0u, a));
+  return cuda_status(launch_pdl(k_prefix_combine, rows, dim3(512), 0, s, 0u, a));
 }
 
 // The kernel's flags, read and cleared: give-up and device check; -1: CUDA error.
