@@ -17,7 +17,8 @@
 // block) and values in stages of 32 keys, each by one instruction of a three-dimensional map: a warp that issues a load
 // waits about 200 clocks before its next, so nine small loads a block held the block at 3750 clocks.  With 64-key
 // blocks (N = 64, A read again for each, 22.6 clocks a key and SM against 17.0) the decode batch below took 529 us against
-// 470, both before pairs walked in step; prefetching blocks into the L2 ahead of the loads gained nothing.
+// 470, both before pairs walked in step.  Prefetching blocks into the L2 ahead of the loads gained 2.5 us for one query
+// behind 131072 rows and cost the other cases 0.2 to 0.4 us: left out.
 // 16 queries of 128 heads behind 131072 rows: 400 us (1460 TFLOP/s, matrix units busy 86% of the time), 478 us when run
 // for seconds, where the power limit holds the clock (1225 TFLOP/s; cuBLAS sustains 1385 there).  64 queries behind 32749
 // rows: 405 us, 481 sustained.  One query of 128 heads behind 131072 rows: 49 us, of which 28 in the loop (5.4 TB/s from

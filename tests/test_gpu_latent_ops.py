@@ -541,6 +541,45 @@ def test_streams_graphs_and_repeats():
     _status_ok()
 
 
+def test_many_streams_at_once():
+    """Calls of different shapes, the sparse attention and the indexer on four streams at a time, each call with its own
+    workspace: the same bytes as alone."""
+    shapes = [(5, 48, 900, [70, 0, 33, 64, 5], 16), (16, 128, 1200, [10 * b for b in range(16)], 64), (1, 128, 7000, [31], 32),
+              (40, 128, 200, None, 16), (3, 16, 100, [1, 0, 200], 8)]
+    cases = [_prefix_case(70 + i, *s) for i, s in enumerate(shapes)]
+    g, B, H, L = _gen(71), 16, 128, 4096
+    kv, q = _randn(g, L, 576).bfloat16(), (2 * _randn(g, B, H, 576)).bfloat16()
+    idx = torch.stack([torch.randperm(L, generator=g, device=DEV)[:256].sort().values for _ in range(B)]).int().contiguous()
+    cnt = torch.full((B,), 256, dtype=torch.int32, device=DEV)
+    qi, w, ki = _randn(g, B, 64, 128).bfloat16(), _randn(g, B, 64), _randn(g, 20000, 128).bfloat16()
+    q_pos = torch.full((B,), 19999, device=DEV)
+
+    def sparse():
+        out = torch.empty(B, H, 512, dtype=torch.bfloat16, device=DEV)
+        lsa.lsa_sparse_attn(q, kv, idx, cnt, 0.04, out, None, lsa.workspace(lsa.lsa_workspace_size(lsa.LSA_OP_ATTN, B, L, 256, H)))
+        return (out,)
+
+    def index():
+        scores = torch.empty(B, 20000, device=DEV)
+        lsa.lsa_index_score(qi, w, ki, q_pos, scores)
+        return (scores,)
+
+    calls = [lambda c=c: _run_prefix(*c, 0.04) for c in cases] + [sparse, index]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for rnd in range(6):
+        got = []
+        for k in range(28):
+            j = (5 * k + rnd) % 7
+            with torch.cuda.stream(streams[(k + rnd) % 4]):
+                got.append((j, calls[j]()))
+        torch.cuda.synchronize()
+        for j, o in got:
+            assert all(torch.equal(x, y) for x, y in zip(o, want[j])), j
+    _status_ok()
+
+
 def test_explicit_stream_and_another_current_device(monkeypatch):
     """A stream given to the call; and a current device that is not the tensors' (as far as one GPU can show it: the calls
     make the tensors' device current and give the same)."""
