@@ -238,7 +238,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(vt_full, 1);
-    start_s[2] = 0;
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
@@ -254,12 +253,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- this pair's part of the line of blocks: thread i sums the tiles [i * per, (i + 1) * per), a scan over the
-  // threads, and the thread that holds the first block finds its tile
+  // ---- this pair's part of the line: its first tile, unit of it, and number of units.  Up to 32 tiles, every warp finds
+  // it alone (a lane a tile); beyond, thread i sums the tiles [i * per, (i + 1) * per) and the warps meet.
+  int tile0 = 0, unit0 = 0, n = 0;
   {
-    int64_t* sums = reinterpret_cast<int64_t*>(mx);
-    const int per = (a.nT + PA_THREADS - 1) / PA_THREADS;
-    const int lo = min(tid * per, a.nT), hi = min(lo + per, a.nT);
+    const int per = a.nT <= 32 ? 1 : (a.nT + PA_THREADS - 1) / PA_THREADS;
+    const int me = a.nT <= 32 ? lane : tid;
+    const int lo = min(me * per, a.nT), hi = min(lo + per, a.nT);
     int64_t mine = 0;
     for (int t = lo; t < hi; ++t) mine += tile_units(a, t);
     int64_t inc = mine;
@@ -268,12 +268,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
       const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    int64_t before = inc - mine, total = 0;
-    for (int w = 0; w < PA_THREADS / 32; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+    int64_t before = inc - mine, total = __shfl_sync(0xffffffffu, inc, 31);
+    if (a.nT > 32) {
+      int64_t* sums = reinterpret_cast<int64_t*>(mx);
+      if (lane == 31) sums[warp] = inc;
+      __syncthreads();
+      total = 0;
+      for (int w = 0; w < PA_THREADS / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+      }
     }
     const int np = static_cast<int>(min(static_cast<int64_t>(PA_PAIRS), total));
     if (pair < np) {
@@ -285,26 +289,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         s0 = total * pair / np;
         s1 = total * (pair + 1) / np;
       }
-      if (s0 >= before && s0 < before + mine) {
+      n = static_cast<int>(s1 - s0);
+      const bool here = s0 >= before && s0 < before + mine;
+      if (a.nT <= 32) {
+        const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        tile0 = src;
+        unit0 = static_cast<int>(s0 - __shfl_sync(0xffffffffu, before, src));
+      } else if (here) {
         int64_t off = s0 - before;
         int t = lo;
-        for (int n = tile_units(a, t); off >= n && t + 1 < hi; n = tile_units(a, t)) {
-          off -= n;
+        for (int k = tile_units(a, t); off >= k && t + 1 < hi; k = tile_units(a, t)) {
+          off -= k;
           ++t;
         }
         start_s[0] = t;
         start_s[1] = static_cast<int>(off);
-        start_s[2] = static_cast<int>(s1 - s0);
       }
     }
-    if (blockIdx.x == 0 && a.own_len)
-      for (int b = tid; b < a.B; b += PA_THREADS)
-        if (a.own_len[b] < 0 || a.own_len[b] > a.cap) atomicExch(&g_prefix_check, 1);
+    // Through shared memory in either case: with the three in the registers that they were found in, the loops of the
+    // matrix instructions came out slower (64 queries behind 32749 rows 406 -> 446 us).
+    if (tid == 0) {
+      if (a.nT <= 32) {
+        start_s[0] = tile0;
+        start_s[1] = unit0;
+      }
+      start_s[2] = n;
+    }
+    __syncthreads();
+    tile0 = start_s[0];
+    unit0 = start_s[1];
+    n = start_s[2];
   }
-  __syncthreads();
-  const int n = start_s[2];
   Cursor c;
-  if (n > 0) c.start(a, start_s[0], start_s[1]);
+  if (n > 0) c.start(a, tile0, unit0);
   bool ok = true;
 
   if (warp == PA_KQ_WARP) {
@@ -757,6 +774,8 @@ struct RowParts {
     i0 = a.multi ? qlo + 2 * t : t;
     i1 = a.multi ? b + 2 * t + 1 : t;
     const int2 g0 = a.seg[i0], g1 = a.seg[i1];
+    const int own = a.own_len ? __ldg(a.own_len + b) : 0;
+    if (own < 0 || own > a.cap) atomicExch(&g_prefix_check, 1);
     const int ob = Cursor::blocks_of(a, b);
     x0 = g0.x;
     x1 = g1.x;
