@@ -58,23 +58,6 @@ __device__ __forceinline__ float2 row_scale(float amax) {
   const float s = amax > 0.f ? amax * (1.f / 448.f) : 1.f;
   return make_float2(s, s > 1e-35f ? __fdividef(1.f, s) : 0.f);
 }
-__device__ __forceinline__ uint32_t codes2(float2 v, float inv) {
-  uint16_t u;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(u) : "f"(v.y * inv), "f"(v.x * inv));
-  return u;
-}
-// the values over the scale where there is no reciprocal: codes are then formed with 1
-template <int N>
-__device__ __forceinline__ float tiny_row(float2 (&f)[N], const float2& sc) {
-  if (sc.y != 0.f) return sc.y;
-  #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = make_float2(f[i].x / sc.x, f[i].y / sc.x);
-  return 1.f;
-}
-__device__ __forceinline__ uint2 codes8(float2 (&f)[4], const float2& sc) {
-  const float inv = tiny_row(f, sc);
-  return make_uint2(codes2(f[0], inv) | (codes2(f[1], inv) << 16), codes2(f[2], inv) | (codes2(f[3], inv) << 16));
-}
 // s / d, off by less than a rounding: the mean of a constant row is that constant (s = c d is exact for a bf16 c)
 __device__ __forceinline__ float mean_of(float s, float d, float inv_d) {
   const float q = s * inv_d;
@@ -107,6 +90,24 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return floats(r);
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ uint32_t codes2(float2 v, float2 inv) {
+  const float2 q = mul2(v, inv);
+  uint16_t u;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(u) : "f"(q.y), "f"(q.x));
+  return u;
+}
+// the values over the scale where there is no reciprocal: codes are then formed with 1
+template <int N>
+__device__ __forceinline__ float tiny_row(float2 (&f)[N], const float2& sc) {
+  if (sc.y != 0.f) return sc.y;
+  #pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = make_float2(f[i].x / sc.x, f[i].y / sc.x);
+  return 1.f;
+}
+__device__ __forceinline__ uint2 codes8(const float2 (&f)[4], float2 inv) {
+  return make_uint2(codes2(f[0], inv) | (codes2(f[1], inv) << 16), codes2(f[2], inv) | (codes2(f[3], inv) << 16));
+}
 
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
@@ -148,7 +149,7 @@ struct NormRopeArgs {
 // 70 at 512; a grid of resident blocks with two tables in turn took 55.
 // 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 45.6 us, 5890 GB/s.  2047 x 128 rows of 64, no norm, into
 // their place in rows of 1152 bytes: 17.4 us cold, 3850 GB/s (128-byte pieces of HBM pages; 11 us in the L2).
-// 4099 x 64 rows of 128, layer norm, to codes: 29.6 us, 3440 GB/s, bound by its instructions (21 an element: three
+// 4099 x 64 rows of 128, layer norm, to codes: 29.6 us, 3440 GB/s, bound by its instructions (about 20 an element: three
 // reductions and a scale a row; 60% of the issue slots at 24 warps an SM, and neither more warps nor larger blocks help).
 template <int G, int ITER, int NORM, bool FP8>
 __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(const NormRopeArgs a) {
@@ -190,19 +191,23 @@ __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(con
   // rows k of the slot's next step: token tl, heads h_first + lh + k spt
   uint4 v[RPT][ITER];
   int tl = tk, lh = 0;
+  const int64_t xstep = spt * a.ldh, ystep = spt * a.yldh;
+  const int64_t xturn = NT * a.ldt - a.HB * a.ldh, yturn = NT * a.yldt - a.HB * a.yldh;  // from a token's end to the next
+  const uint16_t* px = a.x + (t0 + tk) * a.ldt + h_first * a.ldh;
   auto load = [&]() {
-    const uint16_t* px = a.x + (t0 + tl) * a.ldt + (h_first + lh) * a.ldh;
     #pragma unroll
     for (int k = 0; k < RPT; ++k) {
       const bool live = tl < nt && h_first + lh + k * spt < h_end;
       #pragma unroll
       for (int i = 0; i < ITER; ++i)
-        v[k][i] = live && off[i] >= 0 ? *reinterpret_cast<const uint4*>(px + k * spt * a.ldh + off[i]) : make_uint4(0, 0, 0, 0);
+        v[k][i] = live && off[i] >= 0 ? *reinterpret_cast<const uint4*>(px + off[i]) : make_uint4(0, 0, 0, 0);
+      if (k == 0 || lh + spt < a.HB) px += xstep;
     }
     lh += RPT * spt;
     if (lh >= a.HB) {
       lh = 0;
       tl += NT;
+      px += xturn;
     }
   };
   load();
@@ -242,9 +247,10 @@ __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(con
   }
   __syncthreads();
   const float d = static_cast<float>(a.D), inv_d = 1.f / d;
+  int64_t yo = (t0 + tk) * a.yldt + h_first * a.yldh;
+  float* ps = FP8 ? a.scale + (t0 + tk) * a.H + h_first : nullptr;
   for (int tb = 0; tb < a.TB && NT * tb < nt; ++tb) {  // uniform over the block: the shuffles need every lane
     const int tq = NT * tb + tk;
-    const int64_t t = t0 + tq;
     const float4* tab = reinterpret_cast<const float4*>(cs + min(tq, nt - 1) * half_r);  // two pairs an entry
     for (int hb = 0; hb < a.HB; hb += RPT * spt) {
       const int h = h_first + hb, rows = hb + spt < a.HB ? RPT : 1;
@@ -338,7 +344,6 @@ __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(con
           }
         }
       }
-      const int64_t yo = t * a.yldt + h * a.yldh;
       #pragma unroll
       for (int k = 0; k < RPT; ++k) {
         if (k >= rows) break;
@@ -353,21 +358,30 @@ __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(con
             m = fmaxf(m, off[i] >= 0 ? mi : 0.f);
           }
           const float2 sc = row_scale(group_max<G>(m));
+          float inv = sc.y;
+          if (inv == 0.f) {
+            #pragma unroll
+            for (int i = 0; i < ITER; ++i) inv = tiny_row(f[k][i], sc);
+          }
           if (live) {
-            uint8_t* py = static_cast<uint8_t*>(a.y) + yo + k * spt * a.yldh;
+            uint8_t* py = static_cast<uint8_t*>(a.y) + yo;
             #pragma unroll
             for (int i = 0; i < ITER; ++i)
-              if (off[i] >= 0) *reinterpret_cast<uint2*>(py + off[i]) = codes8(f[k][i], sc);
-            if (gl == 0) a.scale[t * a.H + h + k * spt] = sc.x;
+              if (off[i] >= 0) *reinterpret_cast<uint2*>(py + off[i]) = codes8(f[k][i], both(inv));
+            if (gl == 0) ps[k * spt] = sc.x;
           }
         } else if (live) {
-          uint16_t* py = static_cast<uint16_t*>(a.y) + yo + k * spt * a.yldh;
+          uint16_t* py = static_cast<uint16_t*>(a.y) + yo;
           #pragma unroll
           for (int i = 0; i < ITER; ++i)
             if (off[i] >= 0) *reinterpret_cast<uint4*>(py + off[i]) = pack8(f[k][i]);
         }
+        yo += ystep;
       }
+      if (FP8) ps += RPT * spt;
     }
+    yo += yturn;
+    if (FP8) ps += NT * a.H - (a.HB + RPT * spt - 1) / (RPT * spt) * (RPT * spt);
   }
   if (!FP8) {
     __syncthreads();
@@ -540,7 +554,7 @@ __global__ void __launch_bounds__(128, 12) k_cache_append(const AppendArgs a) {
       const float inv = tiny_row(v, sc);
       #pragma unroll
       for (int j = 0; j < 3; ++j)
-        if (at[j] >= 0) store_codes(o + at[j], far[j], codes2(v[j], inv));
+        if (at[j] >= 0) store_codes(o + at[j], far[j], codes2(v[j], both(inv)));
       if (lane == 0) a.k_scale[slot] = sc.x;
     } else if (write) {
       uint16_t* o = static_cast<uint16_t*>(a.kc) + slot * a.d_I;
