@@ -243,6 +243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_pk);
+    tma_prefetch_desc(&tm_pv);
   }
   if (warp == PA_PV_WARP) tmem_alloc_pair(tmem_holder, 512);
   tc_fence_before();
