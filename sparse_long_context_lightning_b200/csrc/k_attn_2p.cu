@@ -465,10 +465,10 @@ __global__ void __launch_bounds__(A2_THREADS, 1)
   // (128-byte rows, 16-byte pieces swizzled by row) so that every store instruction writes four whole
   // 128-byte lines.
   if (warp < A2_GATHER_WARPS || warp >= A2_SOFTMAX_WARP0) {
-    named_bar_sync(2, (A2_GATHER_WARPS + 4) * 32);  // fin_s, have_s; every gather copy has landed
-    if (ntiles == 0 && tid == 0) {
-      for (int kb = 0; kb < A2_QSLOTS; ++kb) (void)mbar_spin(&q_slot[kb], 0, WAIT_NS);  // Q loads of an empty unit
+    if (ntiles == 0 && tid == 0) {  // an empty unit's Q has landed before its staging slots hold the output
+      for (int kb = 0; kb < A2_QSLOTS; ++kb) (void)mbar_spin(&q_slot[kb], 0, WAIT_NS);
     }
+    named_bar_sync(2, (A2_GATHER_WARPS + 4) * 32);  // fin_s, have_s; every gather copy has landed
     const bool have = *reinterpret_cast<volatile int*>(have_s) == 4;
     const int rank = warp < A2_GATHER_WARPS ? warp / 4 : 4;  // this warp's place among its quarter's five
     unsigned char* stg = st_s + (warp < A2_GATHER_WARPS ? warp : warp - 4) * 4096;

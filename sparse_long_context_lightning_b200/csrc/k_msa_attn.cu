@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1)
         (void)mbar_spin(logits ? &lr_full[slot] : &vr_full[slot], (idx / nslot) & 1, WAIT_NS);
       }
     }
+    if (tid == 32) (void)mbar_spin(q_full, 0, WAIT_NS);  // Q's copies too, which an empty group does not read
   } else if (warp == 2 || warp == 3) {
     // ------------------------------------------------------------------ MMA issuers
     if (lane == 0 && ntiles > 0) {
