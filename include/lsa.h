@@ -408,9 +408,8 @@ int lsa_bucket_select_noalloc(const void* q_idx, const float* q_scale, const flo
  *   Kernels: decode-sized batches (every query's rows in units of at most 256, at most 148 units) run one
  *   unit per SM in two passes (logits and softmax, then P.V) and a merge of the units; larger batches run
  *   the value-half kernel.  H < 128 runs the same kernels on zero-padded 128-head queries.  Programmatic
- *   dependent launch: the decode kernel may start loading q while the kernel before it on `stream` is
- *   still running, when that kernel signalled its dependents early (the library's own kernels do, but for
- *   lsa_norm_rope's in bf16, which writes queries); every other input is read after that kernel has completed.
+ *   dependent launch: a kernel may set itself up while the one before it on `stream` is still running; every
+ *   input, q included, is read after that kernel has completed.
  *   q   [B, H, d_qk] bf16;  kv [L, d_qk] bf16 (row stride d_qk);  out [B, H, d_v] bf16;
  *   lse [B, H] fp32 or NULL.  Supported: d_qk = 576, d_v = 512, H in {16, 32, 64, 128},
  *   idx_ld >= max count, max count <= 65536.  q, kv, out 16-byte aligned.

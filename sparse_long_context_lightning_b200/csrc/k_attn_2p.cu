@@ -130,9 +130,9 @@ __device__ __forceinline__ void rescale_o(uint32_t trow, float alpha) {
 
 __global__ void __launch_bounds__(A2_THREADS, 1)
     k_sparse_attn_2p(const __grid_constant__ CUtensorMap tm_q, A2Args a) {
-  // Q, the barriers and TMEM are set up while the previous kernel of the stream may still run (programmatic
-  // dependent launch): Q is an input the pipeline's previous kernels do not write; every other global access
-  // (indices, counts, cache, outputs) comes after pdl_wait()
+  // The barriers and TMEM are set up while the previous kernel of the stream may still run (programmatic dependent
+  // launch).  Every global access comes after pdl_wait(), Q's loads too: the kernel ahead may have written Q (a
+  // rotation of the queries, the padding of their heads), and only behind the wait are its stores promised to be seen.
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* st_s = base;
@@ -168,7 +168,6 @@ __global__ void __launch_bounds__(A2_THREADS, 1)
       mbar_init(&s_empty[i], 4);
       mbar_init(&drain[i], 1);
     }
-    for (int i = 0; i < A2_QSLOTS; ++i) mbar_init(&q_slot[i], 1);
     for (int i = 0; i < A2_MAXT; ++i) {
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
@@ -179,20 +178,24 @@ __global__ void __launch_bounds__(A2_THREADS, 1)
     *abort_flag = 0;
     *have_s = 0;
     fence_mbar_init();
-    // all of Q into the staging slots at once, before the count is known (an empty unit waits for these loads
-    // before it exits)
     tma_prefetch_desc(&tm_q);
-    for (int kb = 0; kb < A2_QSLOTS; ++kb) {
-      mbar_expect_tx(&q_slot[kb], A2_QKB_BYTES);
-      tma_load_2d(q_st + kb * A2_QKB_BYTES, &tm_q, &q_slot[kb], 64 * kb, b * A2_H);
-    }
   }
+  // the warps that do not gather bring Q, a slot or two each, so that no warp issues nine loads in a row
+  const int q_first = lane == 0 && warp >= A2_GATHER_WARPS ? warp - A2_GATHER_WARPS : A2_QSLOTS;
+  constexpr int Q_STEP = A2_THREADS / 32 - A2_GATHER_WARPS;
+  for (int kb = q_first; kb < A2_QSLOTS; kb += Q_STEP) mbar_init(&q_slot[kb], 1);
+  if (q_first < A2_QSLOTS) fence_mbar_init();
   if (warp == A2_LOGIT_WARP0) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
   pdl_wait();
   pdl_launch_dependents();
+  // all of Q into the staging slots, before the count is known (an empty unit waits for these loads before it exits)
+  for (int kb = q_first; kb < A2_QSLOTS; kb += Q_STEP) {
+    mbar_expect_tx(&q_slot[kb], A2_QKB_BYTES);
+    tma_load_2d(q_st + kb * A2_QKB_BYTES, &tm_q, &q_slot[kb], 64 * kb, b * A2_H);
+  }
   // units split the row range by idx_ld (not by count), so the index loads need not wait for the count
   const int T_ld = static_cast<int>((a.idx_ld + A2_T - 1) / A2_T);
   const int t0 = static_cast<int>(static_cast<int64_t>(unit) * T_ld / a.S);

@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(MA_THREADS, 1)
   const int b = bg / 8, hs = bg % 8, g = hs * a.G / 8;
   const int32_t* ridx = a.idx + static_cast<int64_t>(b) * a.ld;
   if (tid == 0) {
-    mbar_init(q_full, 1);
     for (int i = 0; i < MA_LR; ++i) {
       mbar_init(&lr_full[i], 1);
       mbar_init(&lr_empty[i], 1);
@@ -170,19 +169,24 @@ __global__ void __launch_bounds__(MA_THREADS, 1)
     mbar_init(o_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    // Q_g: the group's 16 head rows of query b, nine 64-dim slices (Q is not written by the pipeline's earlier
-    // kernels, so it is loaded before the programmatic-launch wait)
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_kv);
-    mbar_expect_tx(q_full, MA_KB * MA_QSLICE);
-    for (int kb = 0; kb < MA_KB; ++kb) tma_load_2d(qs + kb * 2048, &tm_q, q_full, 64 * kb, b * 128 + hs * MA_NH);
+  }
+  if (tid == 32) {
+    mbar_init(q_full, 1);
+    fence_mbar_init();
   }
   if (warp == 2) {
     tmem_alloc(tmem_holder, 128);
     tmem_relinquish();
   }
+  // every global access comes behind this wait, Q's loads too: the kernel ahead may have written the queries
   pdl_wait();
   pdl_launch_dependents();
+  if (tid == 32) {  // Q_g: the group's 16 head rows of query b, nine 64-dim slices, while warp 0 looks for its tiles
+    mbar_expect_tx(q_full, MA_KB * MA_QSLICE);
+    for (int kb = 0; kb < MA_KB; ++kb) tma_load_2d(qs + kb * 2048, &tm_q, q_full, 64 * kb, b * 128 + hs * MA_NH);
+  }
   if (warp == 0) {
     // this group's tiles: the union row's blocks (entries j * 128 ..) whose mask has bit g, in order
     int n = a.count[b];

@@ -155,10 +155,7 @@ template <int G, int ITER, int NORM, bool FP8>
 __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(const NormRopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin | weight [D] | bias [D]
   sm100::pdl_wait();
-  // A bf16 result may be the query of the decode attention, which reads its query before it waits for this kernel: there
-  // the next kernel starts when every block has ended, with its stores done (2 us of 44 at 8192 x 64 rows).  Codes only go
-  // where they are waited for.
-  if (FP8) sm100::pdl_launch_dependents();
+  sm100::pdl_launch_dependents();
   constexpr int RPT = ITER <= 2 ? 2 : 1;
   const int slot = threadIdx.x / G, gl = threadIdx.x % G;
   const int spt = 1 << a.spt_log, NT = (NR_THREADS / G) >> a.spt_log;
@@ -382,10 +379,6 @@ __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(con
     }
     yo += yturn;
     if (FP8) ps += NT * a.H - (a.HB + RPT * spt - 1) / (RPT * spt) * (RPT * spt);
-  }
-  if (!FP8) {
-    __syncthreads();
-    if (threadIdx.x == 0) __threadfence();  // with the barrier: the block's stores
   }
 }
 
