@@ -461,7 +461,9 @@ int lsa_rope_freqs(int R, double base, int scaling, double factor, int64_t origi
  *     s = mul sin(pos[t] freqs[i]) for pair i < rope_dims / 2 (freqs device fp64 [rope_dims / 2]; NULL: no rotation,
  *     and rope_off, rope_dims, layout, mul and pos are not used)
  *     y + t*y_ldt + h*y_ldh = the D results rounded once to bf16, or (LSA_FP8_E4M3) the e4m3 codes of result / scale
- *     with y_scale[t*H + h] = max |result| / 448 (1 for a row of zeros): the index queries of lsa_index_score.
+ *     with y_scale[t*H + h] = max |result| / 448 (1 for a row of zeros): the index queries of lsa_index_score.  A row with
+ *     a NaN result has a NaN scale and NaN codes; one with an infinite result has an infinite scale, NaN codes for the
+ *     infinities and 0 for the rest: either way the scores that it enters are NaN.
  *   Angles are formed and reduced modulo 2 pi in 64 bits, norm statistics are 32-bit.
  *   x bf16; x_ldt, x_ldh, y_ldt, y_ldh are strides in elements, any multiples of 8 (0 for a broadcast x).  y may be x with
  *   the same strides (bf16); otherwise they must not overlap.  D a multiple of 8, at most 1024; rope_off a multiple of

@@ -51,11 +51,18 @@ __device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
-// The row's scale and its reciprocal (0 where that would overflow).  Codes are formed from value * reciprocal: a quotient
+// The larger of two, NaN if either is: a NaN has to reach the row's scale, since the indexer's ReLU takes a NaN product of
+// codes for 0 and only the scale then carries it into the score.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The row's scale and its reciprocal (0 where that would overflow, and for an infinite or NaN scale).  Codes are formed from value * reciprocal: a quotient
 // takes ten instructions an element, and the product, off by two roundings of 32 bits, can only choose another code for a
 // value within 2^-22 of the border of two, where the norm's own rounding chooses as much.
 __device__ __forceinline__ float2 row_scale(float amax) {
-  const float s = amax > 0.f ? amax * (1.f / 448.f) : 1.f;
+  const float s = amax == 0.f ? 1.f : amax * (1.f / 448.f);
   return make_float2(s, s > 1e-35f ? __fdividef(1.f, s) : 0.f);
 }
 // s / d, off by less than a rounding: the mean of a constant row is that constant (s = c d is exact for a bf16 c)
@@ -118,7 +125,7 @@ __device__ __forceinline__ float group_sum(float v) {
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
   #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = G / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -351,8 +358,8 @@ __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(con
           for (int i = 0; i < ITER; ++i) {
             float mi = 0.f;
             #pragma unroll
-            for (int j = 0; j < 4; ++j) mi = fmaxf(mi, fmaxf(fabsf(f[k][i][j].x), fabsf(f[k][i][j].y)));
-            m = fmaxf(m, off[i] >= 0 ? mi : 0.f);
+            for (int j = 0; j < 4; ++j) mi = max_nan(mi, max_nan(fabsf(f[k][i][j].x), fabsf(f[k][i][j].y)));
+            m = max_nan(m, off[i] >= 0 ? mi : 0.f);
           }
           const float2 sc = row_scale(group_max<G>(m));
           float inv = sc.y;
@@ -540,8 +547,8 @@ __global__ void __launch_bounds__(128, 12) k_cache_append(const AppendArgs a) {
     if (FP8) {
       float m = 0.f;
       #pragma unroll
-      for (int j = 0; j < 3; ++j) m = fmaxf(m, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
-      const float2 sc = row_scale(warp_max(m));
+      for (int j = 0; j < 3; ++j) m = max_nan(m, max_nan(fabsf(v[j].x), fabsf(v[j].y)));
+      const float2 sc = row_scale(group_max<32>(m));
       if (!write) return;
       uint8_t* o = static_cast<uint8_t*>(a.kc) + slot * a.d_I;
       const float inv = tiny_row(v, sc);

@@ -267,6 +267,105 @@ def test_cache_append_past_32_bit_offsets():
     assert torch.equal(kv[[n - 1, n - 3]], a) and not kv[:4].any() and not kv[[n - 2, n - 4]].any()
 
 
+# ------------------------------------------------------------------------------------------------ values that are not finite
+
+
+def _with_bad_rows(g, T, H, D):
+    """Rows 0, 3, 6 .. hold one NaN, rows 1, 4 .. one infinity of either sign, the others are ordinary."""
+    x = _randn(g, T, H, D).bfloat16()
+    x[0::3, :, 5] = math.nan
+    x[1::3, :, D - 1] = math.inf
+    x[4::6, :, D - 1] = -math.inf
+    return x
+
+
+@pytest.mark.parametrize("norm", ["none", "rms", "layer"])
+@pytest.mark.parametrize("D,H,R", [(128, 64, 64), (24, 3, 16), (1024, 1, 0)])
+def test_norm_rope_values_that_are_not_finite(norm, D, H, R):
+    """A NaN reaches its whole row's codes and their scale, an infinity the scale; in bf16 every element is what the
+    formula gives; other rows are as always."""
+    T = 13
+    x = _with_bad_rows(_gen(D), T, H, D)
+    pos = torch.arange(T, device=DEV) * 1000
+    freqs, mul = lsa.lsa_rope_freqs(R) if R else (None, 1.0)
+    want = norm64(x, norm, None, None, 1e-6)
+    if R:
+        want = rotate64(want, pos, freqs, 0, "half", mul)
+    kw = dict(norm=norm, layout="half") if R == 0 else dict(pos=pos, freqs=freqs, norm=norm, layout="half", mul=mul)
+    y = torch.empty_like(x)
+    lsa.lsa_norm_rope(x, y, **kw)
+    assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.isinf(), want.isinf())
+    fine = torch.isfinite(x.float()).all(-1).all(-1)
+    check_rows(y[fine], want[fine], mul)
+    c, sc = torch.empty(T, H, D, dtype=torch.uint8, device=DEV), torch.empty(T, H, device=DEV)
+    lsa.lsa_norm_rope(x, c, y_scale=sc, **kw)
+    v = c.view(torch.float8_e4m3fn).float()
+    check_codes(c[fine], sc[fine], want[fine], mul)
+    top = want.abs().amax(-1)  # NaN where the row has one
+    assert torch.equal(sc.isnan(), top.isnan()) and torch.equal(sc.isinf(), top.isinf())
+    assert bool(v[top.isnan()].isnan().all())
+    inf = top.isinf()
+    assert torch.equal(v[inf].isnan(), want[inf].isinf()) and not v[inf][~want[inf].isinf()].any()
+
+
+@pytest.mark.parametrize("k_norm", ["none", "rms", "layer"])
+@pytest.mark.parametrize("d_I", [32, 128])
+def test_cache_append_values_that_are_not_finite(k_norm, d_I):
+    """The same for the rows of both caches."""
+    g, T = _gen(d_I + 1), 13
+    a, k = _with_bad_rows(g, T, 1, 576)[:, 0], _with_bad_rows(g, T, 1, d_I)[:, 0].contiguous()
+    k_off = 0 if d_I >= 64 else -1
+    pos, slot = torch.arange(T, device=DEV) * 1000, torch.randperm(T, generator=g, device=DEV)
+    freqs, mul = lsa.lsa_rope_freqs(64)
+    wa = 1 + 0.2 * _randn(g, 512)
+    want_a = torch.cat([norm64(a[:, :512], "rms", wa, None, 1e-6), rotate64(a[:, 512:].double(), pos, freqs, 0, "half", mul)], 1)
+    want = norm64(k, k_norm, None, None, 1e-6)
+    if k_off >= 0:
+        want = rotate64(want, pos, freqs, k_off, "half", mul)
+    fine = torch.isfinite(a.float()).all(-1) & torch.isfinite(k.float()).all(-1)
+    for fp8 in (False, True):
+        kv = torch.zeros(T, 576, dtype=torch.bfloat16, device=DEV)
+        kc = torch.zeros(T, d_I, dtype=torch.uint8 if fp8 else torch.bfloat16, device=DEV)
+        ks = torch.zeros(T, device=DEV) if fp8 else None
+        lsa.lsa_cache_append(a, kv, slot, pos, freqs, kv_weight=wa, layout="half", mul=mul, k=k, k_cache=kc, k_scale=ks,
+                             k_norm=k_norm, k_rope_off=k_off)
+        got = kv[slot]
+        assert torch.equal(got.isnan(), want_a.isnan()) and torch.equal(got.isinf(), want_a.isinf())
+        check_rows(got[fine], want_a[fine], mul)
+        if not fp8:
+            got = kc[slot]
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+            check_rows(got[fine], want[fine], mul)
+            continue
+        sc, v = ks[slot], kc[slot].view(torch.float8_e4m3fn).float()
+        check_codes(kc[slot][fine], sc[fine], want[fine], mul)
+        top = want.abs().amax(-1)
+        assert torch.equal(sc.isnan(), top.isnan()) and torch.equal(sc.isinf(), top.isinf())
+        assert bool(v[top.isnan()].isnan().all())
+        inf = top.isinf()
+        assert torch.equal(v[inf].isnan(), want[inf].isinf()) and not v[inf][~want[inf].isinf()].any()
+
+
+def test_index_scores_of_codes_that_are_not_finite():
+    """A NaN or infinite index key, or query, gives NaN scores and not a finite one that could pass for an unrelated key."""
+    g, L, H = _gen(81), 300, 16
+    k, qi = _randn(g, L, 128).bfloat16(), _randn(g, 3, H, 128).bfloat16()
+    k[7, 3], k[200, 90], qi[1, 5, 64] = math.nan, math.inf, math.nan
+    for norm in ("none", "layer"):
+        kc, ks = torch.zeros(L, 128, dtype=torch.uint8, device=DEV), torch.zeros(L, device=DEV)
+        at = torch.arange(L, device=DEV)
+        a, kv = torch.zeros(L, 576, dtype=torch.bfloat16, device=DEV), torch.zeros(L, 576, dtype=torch.bfloat16, device=DEV)
+        lsa.lsa_cache_append(a, kv, at, k=k, k_cache=kc, k_scale=ks, k_norm=norm)
+        qc, qs = torch.empty(3, H, 128, dtype=torch.uint8, device=DEV), torch.empty(3, H, device=DEV)
+        lsa.lsa_norm_rope(qi, qc, norm="rms", y_scale=qs)
+        scores = torch.empty(3, L, device=DEV)
+        lsa.lsa_index_score(qc, _randn(g, 3, H), kc, torch.full((3,), L - 1, device=DEV), scores, q_scale=qs, k_scale=ks)
+        assert bool(scores[1].isnan().all())
+        ok = torch.ones(L, dtype=torch.bool, device=DEV)
+        ok[[7, 200]] = False
+        assert bool(scores[[0, 2]][:, ~ok].isnan().all()) and bool(torch.isfinite(scores[[0, 2]][:, ok]).all())
+
+
 # ------------------------------------------------------------------------------------------------ prefix_attn
 
 
