@@ -611,11 +611,12 @@ const char* lsa_version(void);
  *   (2 s of globaltimer); a wait that runs out sets a device flag, the kernel's other roles stop at their next
  *   wait, the issuing threads wait (bounded) for the copies and MMAs they started, TMEM is freed and the
  *   outputs of that launch are not valid.  The decode attention kernel also checks every selected index
- *   against [0, L): an index outside it is clamped (the access stays in bounds) and flagged.
- *   This call synchronises `stream`, then reads and clears the flags: LSA_ERR_TIMEOUT if a wait gave up since
- *   the previous call, else LSA_ERR_DEVICE_CHECK if an index check failed (lsa_last_error names the kernel),
- *   LSA_ERR_CUDA if the stream or the flag read failed, else LSA_OK.  Not part of the hot path (it blocks the
- *   host); meant for a serving loop's periodic health check.
+ *   against [0, L): an index outside it is clamped (the access stays in bounds) and flagged; so do lsa_prefix_attn
+ *   its lengths and page ids and lsa_cache_append its slots.
+ *   This call synchronises `stream`, then reads and clears the current GPU's flags: LSA_ERR_TIMEOUT if a wait gave
+ *   up since the previous call, else LSA_ERR_DEVICE_CHECK if a check failed (lsa_last_error names every kernel that
+ *   set a flag of either kind), LSA_ERR_CUDA if the stream or the flag read failed, else LSA_OK.  Not part of the hot
+ *   path (it blocks the host); meant for a serving loop's periodic health check.
  */
 int lsa_device_status(void* stream);
 

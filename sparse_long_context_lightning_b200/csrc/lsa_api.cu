@@ -7,7 +7,7 @@
 
 namespace lsa {
 
-static thread_local char g_last_error[256] = "";
+static thread_local char g_last_error[1024] = "";  // every flag of lsa_device_status at once takes about 600
 
 void set_last_error(const char* msg) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s", msg ? msg : "");
@@ -188,34 +188,42 @@ int lsa_device_status(void* stream) {
   const int pa = take_prefix_flags(&pa_check), ap_check = take_append_check();
   if (ix < 0 || at < 0 || rs < 0 || a2 < 0 || stw < 0 || sm_check < 0 || tt < 0 || ma < 0 || pa < 0 || ap_check < 0)
     return cuda_status(cudaGetLastError());
-  if (ix || at || rs || a2 || stw || tt || ma || pa) {
-    char msg[256];
-    std::snprintf(msg, sizeof(msg), "bounded wait gave up in:%s%s%s%s%s%s%s%s", ix ? " k_index_score_tc" : "",
-                  at ? " k_sparse_attn_tc" : "", rs ? " k_rescore_tc" : "", a2 ? " k_sparse_attn_2p" : "",
-                  stw ? " k_selftest_wait" : "", tt ? " k_tree_child_tc" : "", ma ? " k_msa_attn_rows" : "",
-                  pa ? " k_prefix_attn" : "");
-    set_last_error(msg);
-    return LSA_ERR_TIMEOUT;
+  // Every flag was cleared above, so the message names all that were set, whatever the status.
+  const bool gave_up = ix || at || rs || a2 || stw || tt || ma || pa;
+  const bool selected = a2_check || at_check || sm_check || ma_check;
+  if (!gave_up && !selected && !pa_check && !ap_check) return LSA_OK;
+  char msg[sizeof(g_last_error)] = "";
+  auto add = [&](bool yes, const char* text) {
+    if (yes) std::strncat(msg, text, sizeof(msg) - 1 - std::strlen(msg));
+  };
+  if (gave_up) {
+    add(true, "bounded wait gave up in:");
+    add(ix, " k_index_score_tc");
+    add(at, " k_sparse_attn_tc");
+    add(rs, " k_rescore_tc");
+    add(a2, " k_sparse_attn_2p");
+    add(stw, " k_selftest_wait");
+    add(tt, " k_tree_child_tc");
+    add(ma, " k_msa_attn_rows");
+    add(pa, " k_prefix_attn");
   }
-  if (a2_check || at_check || sm_check || ma_check) {
-    char msg[256];
-    std::snprintf(msg, sizeof(msg),
-                  "device check failed (a selected index outside [0, L), the row clamped; or MSA rows that are not whole "
-                  "blocks) in:%s%s%s%s",
-                  a2_check ? " k_sparse_attn_2p" : "", at_check ? " k_sparse_attn_tc" : "",
-                  sm_check ? " k_attn_simt" : "", ma_check ? " k_msa_attn_rows" : "");
-    set_last_error(msg);
-    return LSA_ERR_DEVICE_CHECK;
+  if (selected) {
+    add(gave_up, "; ");
+    add(true, "device check failed (a selected index outside [0, L), the row clamped; or MSA rows that are not whole "
+              "blocks) in:");
+    add(a2_check, " k_sparse_attn_2p");
+    add(at_check, " k_sparse_attn_tc");
+    add(sm_check, " k_attn_simt");
+    add(ma_check, " k_msa_attn_rows");
   }
   if (pa_check || ap_check) {
-    char msg[256];
-    std::snprintf(msg, sizeof(msg), "device check failed in:%s%s",
-                  pa_check ? " k_prefix_attn (own_len outside [0, table columns * page], or a bad page id)" : "",
-                  ap_check ? " k_cache_append (a slot outside [-1, n_slots); the row was skipped)" : "");
-    set_last_error(msg);
-    return LSA_ERR_DEVICE_CHECK;
+    add(gave_up || selected, "; ");
+    add(true, "device check failed in:");
+    add(pa_check, " k_prefix_attn (own_len outside [0, table columns * page], or a bad page id)");
+    add(ap_check, " k_cache_append (a slot outside [-1, n_slots); the row was skipped)");
   }
-  return LSA_OK;
+  set_last_error(msg);
+  return gave_up ? LSA_ERR_TIMEOUT : LSA_ERR_DEVICE_CHECK;
 }
 
 const char* lsa_last_error(void) { return g_last_error; }

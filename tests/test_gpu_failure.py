@@ -100,3 +100,45 @@ def test_msa_rows_that_are_not_whole_blocks_are_reported():
     assert e.value.status == LSA_ERR_DEVICE_CHECK
     assert b"k_msa_attn_rows" in lsa.load_library().lsa_last_error()
     lsa.lsa_device_status()  # the flag was cleared
+
+
+def test_every_report_since_the_last_call_is_named():
+    """Flags of several kernels in one interval: a wait that gave up, a bad selected index, a slot outside the cache and a
+    bad page id.  One call reads and clears them all, so its message names them all; without the wait the status is the
+    checks'."""
+    L, H = 500, 128
+    kv = S.normal_bf16(S.ST_KV, (L, 576), DEV)
+    q = S.normal_bf16(S.ST_Q, (2, H, 576), DEV)
+    out = torch.empty(2, H, 512, dtype=torch.bfloat16, device=DEV)
+    idx = torch.full((2, 32), 7, dtype=torch.int32, device=DEV)
+    idx[1, 3] = L
+    cnt = torch.full((2,), 32, dtype=torch.int32, device=DEV)
+    ws = lsa.workspace(lsa.lsa_workspace_size(lsa.LSA_OP_ATTN, 2, L, 32, H))
+    pages = kv[:64].reshape(4, 16, 576).contiguous()
+    table = torch.tensor([[0], [4]], dtype=torch.int32, device=DEV)  # page 4 of 4
+    own = torch.tensor([3, 3], dtype=torch.int32, device=DEV)
+    pws = lsa.workspace(lsa.lsa_prefix_attn_workspace_size(2, H))
+
+    def select():
+        lsa.lsa_sparse_attn(q, kv, idx, cnt, 0.04, out, None, ws)
+
+    def page():
+        lsa.lsa_prefix_attn(q, kv, 0.04, out, pages=pages, table=table, own_len=own, ws=pws)
+
+    def slot():
+        lsa.lsa_cache_append(kv[:3].clone(), kv, torch.tensor([1, L, 2], device=DEV))
+
+    calls = {"k_selftest_wait": lambda: lsa.lsa_selftest_wait(1_000_000), "k_sparse_attn_2p": select, "k_prefix_attn": page,
+             "k_cache_append": slot}
+    lsa.lsa_device_status()  # clean start
+    names = list(calls)
+    for chosen in ([0, 1, 2, 3], [1, 2, 3], [0, 3], [0, 2], [1, 3], [1, 2], [2, 3], [0, 1]):
+        for i in chosen:
+            calls[names[i]]()
+        with pytest.raises(lsa.LsaError) as e:
+            lsa.lsa_device_status()
+        assert e.value.status == (LSA_ERR_TIMEOUT if 0 in chosen else LSA_ERR_DEVICE_CHECK)
+        said = lsa.load_library().lsa_last_error().decode()
+        assert [n for n in names if n in said] == [names[i] for i in chosen], said
+        assert said in str(e.value)
+        lsa.lsa_device_status()  # all were cleared
