@@ -794,13 +794,12 @@ __device__ __forceinline__ uint2 pack4(const float4& v, float inv) {
   const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv), hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
+// (every partial that is joined was written, and one of weight 0 counts too: 0 times an infinity is the formula's NaN)
 __device__ __forceinline__ void add_part(float4& acc, float w, const float4& v) {
-  if (w != 0.f) {  // a partial without keys holds nothing
-    acc.x += w * v.x;
-    acc.y += w * v.y;
-    acc.z += w * v.z;
-    acc.w += w * v.w;
-  }
+  acc.x += w * v.x;
+  acc.y += w * v.y;
+  acc.z += w * v.z;
+  acc.w += w * v.w;
 }
 
 // Many rows: a warp each, 16 columns a lane, a partial's maximum and sum a lane.

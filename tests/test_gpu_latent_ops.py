@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import sparse_long_context_lightning_b200 as lsa
-from latent_common import check_codes, check_prefix, check_rows, norm64, rotate64
+from latent_common import check_codes, check_prefix, check_rows, norm64, prefix64, rotate64
 from oracle import lsa_oracle as O
 
 pytestmark = pytest.mark.gpu
@@ -500,6 +500,32 @@ def test_prefix_attn_a_non_finite_sequence_stays_its_own():
     out, lse = _run_prefix(q, prefix, pages, table, own, 0.04)
     check_prefix(out, lse, q, prefix, 0.04, pages, table, own, rows=[0, 2, 3])
     assert not torch.isfinite(out[1].float()).all()
+
+
+@pytest.mark.parametrize("B,H,L", [(1, 16, 20000), (1, 128, 20000), (1, 300, 3000), (3, 128, 9000), (40, 128, 9000), (3, 48, 9000)])
+def test_prefix_attn_infinite_values_of_keys_that_weigh_nothing(B, H, L):
+    """A key with an infinite element and a logit of -inf, among keys whose weights underflow: the column is NaN (0 times
+    infinity) in every row, wherever the work was cut, and the other columns and the sums are ordinary."""
+    g = _gen(90 + B)
+    q = (0.2 * _randn(g, B, H, 576)).bfloat16()
+    q[:, :, 5], q[:, :, 7] = 1.0, 8.0
+    prefix = _randn(g, L, 576).bfloat16()
+    prefix[:, 7] = 0
+    prefix[: L // 3, 7] = -60.0  # logits 480 below the others
+    prefix[3, 5] = -math.inf
+    out, lse = _run_prefix(q, prefix, None, None, None, 1.0)
+    assert bool(out[:, :, 5].isnan().all())
+    other = [d for d in range(512) if d != 5]
+    clean = prefix[torch.arange(L, device=DEV) != 3]
+    # Column 7 is -60 times weights of e^-480: in 32 bits a weight below 2^-126 may be 0, so up to 2^15 keys of magnitude
+    # up to 2^6 lose up to 2^-126 * 2^15 * 2^6 = 2^-105 of a sum whose largest weight is 1 (it is divided by 1 or more).
+    lost = 2.0 ** -105
+    for b in range(0, B, 13):
+        o, l, mag, dz = prefix64(q, clean, 1.0, None, None, None, b)
+        tol = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.1 * dz + 2.0 ** -12) * mag * (1 + 2.0 ** -8) + lost
+        assert ((out[b].double() - o).abs() <= tol)[:, other].all()
+        assert ((lse[b].double() - l).abs() <= dz + 2.0 ** -18 * (1 + l.abs())).all()
+    _status_ok()
 
 
 def test_prefix_attn_shared_pages_and_speculative_tokens():
