@@ -465,8 +465,8 @@ int lsa_rope_freqs(int R, double base, int scaling, double factor, int64_t origi
  *     a NaN result has a NaN scale and NaN codes; one with an infinite result has an infinite scale, NaN codes for the
  *     infinities and 0 for the rest: either way the scores that it enters are NaN.
  *   Angles are formed and reduced modulo 2 pi in 64 bits, norm statistics are 32-bit.
- *   x bf16; x_ldt, x_ldh, y_ldt, y_ldh are strides in elements, any multiples of 8 (0 for a broadcast x).  y may be x with
- *   the same strides (bf16); otherwise they must not overlap.  D a multiple of 8, at most 1024; rope_off a multiple of
+ *   x bf16; x_ldt, x_ldh, y_ldt, y_ldh are strides in elements, any multiples of 8 (0 for a broadcast x).  Rows of y that
+ *   overlap each other are refused.  y may be x with the same strides (bf16); otherwise they must not overlap.  D a multiple of 8, at most 1024; rope_off a multiple of
  *   8, rope_dims of 16.  x 16-byte aligned, y 16 bytes (bf16) or 8 (e4m3).  y_scale non-NULL for LSA_FP8_E4M3 only.
  */
 int lsa_norm_rope(const void* x, int64_t x_ldt, int64_t x_ldh, int64_t T, int H, int D, int norm, const float* weight,

@@ -1,6 +1,7 @@
 // C ABI of the library: argument validation, scratch layout, dispatch to the kernels.
 #include <cstdio>
 #include <cstring>
+#include <utility>
 
 #include "lsa_common.cuh"
 #include "sm100.cuh"
@@ -665,6 +666,25 @@ int lsa_rope_freqs(int R, double base, int scaling, double factor, int64_t origi
   return LSA_OK;
 }
 
+// Whether two of the n0 x n1 rows of D elements that begin at multiples of the strides s0, s1 share an element: two rows i
+// and j apart along the axes do where |i s0 + j s1| < D.  (Along the longer stride at most s0 / D steps stay apart from
+// every multiple of the shorter one, so the loop is short; its bound is for strides that no tensor has.)
+static bool rows_overlap(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int D) {
+  typedef __int128 wide;
+  wide a = s0 < 0 ? -static_cast<wide>(s0) : s0, b = s1 < 0 ? -static_cast<wide>(s1) : s1;
+  if ((n0 > 1 && a < D) || (n1 > 1 && b < D)) return true;
+  if (n0 <= 1 || n1 <= 1) return false;
+  if (a > b) {
+    std::swap(a, b);
+    std::swap(n0, n1);
+  }
+  for (int64_t j = 1; j < n1 && j <= 65536 && j * b < a * (n0 - 1) + D; ++j) {
+    const wide d = j * b, i = d / a;
+    if ((i < n0 && d - i * a < D) || (i + 1 < n0 && (i + 1) * a - d < D)) return true;
+  }
+  return false;
+}
+
 int lsa_norm_rope(const void* x, int64_t x_ldt, int64_t x_ldh, int64_t T, int H, int D, int norm, const float* weight,
                   const float* bias, float eps, const double* freqs, int rope_off, int rope_dims, int layout, float mul,
                   const int64_t* pos, void* y, int64_t y_ldt, int64_t y_ldh, int dtype, float* y_scale, void* stream) {
@@ -685,6 +705,7 @@ int lsa_norm_rope(const void* x, int64_t x_ldt, int64_t x_ldh, int64_t T, int H,
   LSA_CHECK_ARG(x && y && (freqs == nullptr || pos));
   LSA_CHECK_ARG(aligned16(x) && (reinterpret_cast<uintptr_t>(y) & (dtype == LSA_BF16 ? 15u : 7u)) == 0);
   LSA_CHECK_ARG(x_ldt % 8 == 0 && x_ldh % 8 == 0 && y_ldt % 8 == 0 && y_ldh % 8 == 0);
+  LSA_CHECK_ARG(!rows_overlap(y_ldt, T, y_ldh, H, D));
   return launch_norm_rope(x, x_ldt, x_ldh, T, H, D, norm, weight, bias, eps, freqs, rope_off, rope_dims, layout, mul, pos,
                           y, y_ldt, y_ldh, dtype, y_scale, static_cast<cudaStream_t>(stream));
 }

@@ -133,6 +133,27 @@ def test_norm_rope_strides_and_in_place():
                 assert torch.equal(x[..., :512], before[..., :512])
 
 
+@pytest.mark.parametrize("T,H,t,h", [(3, 2, 2 * 64, 3 * 64), (5, 4, 64, 5 * 64), (4, 5, 5 * 64, 64), (2, 3, 64, 200),
+                                     (7, 2, 208, 72), (1, 6, 0, 64), (6, 1, 64, 0)])
+def test_norm_rope_interleaved_outputs(T, H, t, h):
+    """Rows of y that lie between each other without sharing an element are written; what lies between them stays."""
+    g, D = _gen(T + h), 64
+    at = torch.tensor(sorted(i * t + j * h for i in range(T) for j in range(H)))
+    assert T * H == 1 or int((at[1:] - at[:-1]).min()) >= D
+    flat = _randn(g, int(at.max()) + D + 40).bfloat16()
+    before, x = flat.clone(), _randn(g, T, H, D).bfloat16()
+    y = flat.as_strided((T, H, D), (t, h, 1))
+    freqs, mul = lsa.lsa_rope_freqs(64)
+    pos = torch.arange(T, device=DEV)
+    lsa.lsa_norm_rope(x, y, pos, freqs, norm="rms")
+    check_rows(y, rotate64(norm64(x, "rms", None, None, 1e-6), pos, freqs, 0, "interleaved", mul))
+    rest = torch.ones_like(flat, dtype=torch.bool)
+    rest.as_strided((T, H, D), (t, h, 1)).fill_(False)
+    assert torch.equal(flat[rest], before[rest])
+    with pytest.raises(lsa.LsaError):
+        lsa.lsa_norm_rope(x.expand(T, H, D).repeat(1, 2, 1), flat.as_strided((T, 2 * H, D), (t or 8, 32, 1)), pos, freqs)
+
+
 def test_norm_rope_refusals():
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device=DEV)
     y, freqs = torch.empty_like(x), lsa.lsa_rope_freqs(64)[0]

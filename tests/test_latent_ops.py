@@ -61,6 +61,19 @@ def test_norm_rope_refusals(lib, kw, want):
     assert _norm_rope(lib, **kw) == want
 
 
+@pytest.mark.parametrize("kw", [
+    dict(y_ldh=64), dict(y_ldh=-120), dict(y_ldh=0), dict(y_ldt=0), dict(y_ldt=120), dict(y_ldt=128), dict(y_ldt=8064),
+    dict(y_ldt=-256, y_ldh=128), dict(T=4, H=3, y_ldt=256, y_ldh=384), dict(T=8, H=8, y_ldt=136, y_ldh=1000),
+    dict(T=1, y_ldh=64), dict(H=1, y_ldt=64), dict(T=1 << 40, y_ldt=1 << 30, y_ldh=1 << 30)])
+def test_norm_rope_refuses_outputs_that_overlap_themselves(lib, kw):
+    """Two rows of y that share elements: which row's results stay would depend on the order of the blocks."""
+    a = dict(dict(T=4, H=64, y_ldt=8192, y_ldh=128), **kw)
+    if a["T"] < 100:  # by the definition: some two begin less than a row apart (the call would be launched otherwise)
+        at = sorted(i * a["y_ldt"] + j * a["y_ldh"] for i in range(a["T"]) for j in range(a["H"]))
+        assert min(v - u for u, v in zip(at, at[1:])) < 128
+    assert _norm_rope(lib, **kw) == INVALID
+
+
 def _append(lib, **kw):
     a = dict(a=FAKE, a_ld=576, T=4, d_qk=576, d_v=512, kv_weight=FAKE, kv_eps=1e-6, freqs=FAKE, layout=0, mul=1.0,
              pos=FAKE, slot=FAKE, kv=FAKE, n_slots=64, k=FAKE, k_ld=128, d_I=128, k_norm=2, k_weight=FAKE, k_bias=FAKE,
