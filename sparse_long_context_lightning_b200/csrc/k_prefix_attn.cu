@@ -76,7 +76,7 @@ struct PaArgs {
   int kbox, vbox;  // rows of a page box: min(page, 64 or 32) of keys, min(page, 32) of values
   int n_pages;
   int cap;  // most own tokens: the table's columns * page (clamped to int)
-  int B, H;
+  int H;
   int64_t BH;
   int nT;     // tiles
   int multi;  // tiles may hold rows of several queries
@@ -883,8 +883,9 @@ __global__ void __launch_bounds__(128) k_prefix_combine_warps(const PaArgs a) {
 }
 
 // Few rows, so many partials each (up to 74): four blocks a row, 128 columns a block; 16 warps take the partials in turn,
-// every load of a row on its way before the weights are formed.  The whole call against one block a row (below): 64 rows
-// of 74 partials 17.8 against 20.2 us, 128 rows of 64 17.4 against 18.1, of 48 17.2 against 16.8, of 8 14.9 against 13.6.
+// every load of a row on its way before the weights are formed.  The whole call against one block a row (below), in a
+// graph: 128 rows of 74 partials 16.9 against 18.1 us, of 56 16.2 against 17.1, of 48 16.0 against 16.6, of 40 16.0 against
+// 15.2, of 8 14.0 against 12.8; 64 rows of 74 16.0 against 18.5, of 48 15.5 against 16.0.
 __global__ void __launch_bounds__(512) k_prefix_combine_few(const PaArgs a) {
   constexpr int W = 16, U = 5;
   __shared__ float wt[2 * PA_PAIRS];
@@ -1066,7 +1067,6 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   a.vbox = page < PA_VT ? page : PA_VT;
   a.n_pages = static_cast<int>(n_pages);
   a.cap = static_cast<int>(table_ld * page < 0x7FFFFF00 ? table_ld * page : 0x7FFFFF00);
-  a.B = static_cast<int>(B);
   a.H = H;
   a.BH = B * H;
   a.nT = static_cast<int>(p.nT);
@@ -1093,8 +1093,10 @@ int launch_prefix_attn(const void* q, int64_t B, int H, const void* prefix, int6
   LSA_CUDA_TRY(func_smem_once(reinterpret_cast<const void*>(k_prefix_attn), PA_SMEM));
   LSA_CUDA_TRY(launch_pdl(k_prefix_attn, dim3(2 * PA_PAIRS), dim3(PA_THREADS), PA_SMEM, s, 0u, tq, tk, tv, tpk, tpv, a));
   // About how many partials a row has chooses the join.  Few: a warp for 128 columns, against a block a row: 4 tiles of 18
-  // partials 33.5 against 34.6 us, 8 of 9 43.7 against 50.2, one of 8 12.8 against 13.2; 3 tiles of 25 32.5 against 31.3,
-  // one of 12 14.0 against 13.2.  Many tiles, most rows written already: a warp a row (74 tiles 48.8 us against 54.8).
+  // partials 33.5 against 34.6 us, 8 of 9 43.7 against 50.2, one of 8 12.6 against 12.8; one of 12 13.8 against 12.9, of 32
+  // 18.2 against 14.6, two of 10 14.0 against 13.3, three of 25 19.7 against 18.4 (of 16 15.4 against 16.0: the rule takes
+  // no account of three).  Many tiles, most rows written already: a warp a row (74 tiles 48.8 us against 54.8).  The lengths
+  // of own tokens are not known here: where those take most of the pairs, the prefix has fewer partials than this counts.
   const int64_t blocks = a.nP + (own_len && !a.multi ? cdiv(a.cap, PA_T) : 0);  // of a tile, at most
   const int64_t parts = std::min<int64_t>(blocks, PA_PAIRS / std::min(a.nT, PA_PAIRS)) + (a.multi ? 1 : 0);
   const dim3 rows(static_cast<unsigned>(a.BH));
