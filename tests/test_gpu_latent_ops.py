@@ -449,6 +449,22 @@ def test_prefix_attn_many_tiles(B, H, Lp, lens, page):
     _status_ok()
 
 
+@pytest.mark.parametrize("B,H,Lp,lens,page", [
+    (400, 128, 130, [b % 3 for b in range(400)], 16), (300, 33, 70, [(7 * b) % 40 for b in range(300)], 8),
+    (150, 48, 0, [(29 * b) % 300 for b in range(150)], 128), (6, 64, 3000, [1500, 0, 0, 700, 1, 129], 64),
+    (2, 130, 777, [260, 3], 16), (80, 128, 127, None, 0), (70, 8, 0, [0] * 70, 8)])
+def test_prefix_attn_every_row_is_written_and_finite(B, H, Lp, lens, page):
+    """Outputs that held NaN, beside pages that hold NaN behind each sequence's end: every element of every row is finite,
+    and a row without keys is zeros with lse -inf."""
+    q, prefix, pages, table, own = _prefix_case(B * 3 + H, B, H, Lp, lens, page)
+    out, lse = _run_prefix(q, prefix, pages, table, own, 0.04)
+    assert bool(torch.isfinite(out.float()).all())
+    none = torch.zeros(B, dtype=torch.bool, device=DEV) if Lp or lens is None else own == 0
+    assert not out[none].any() and bool((lse[none] == -math.inf).all()) and bool(torch.isfinite(lse[~none]).all())
+    assert bool(out[~none].abs().amax(-1).gt(0).all())
+    _status_ok()
+
+
 def test_prefix_attn_past_32_bit_offsets():
     """A prefix of more than 2^32 bytes and 2^31 elements: rows of zeros (logit 0, value 0) but for the last 300."""
     g, B, H, L, n = _gen(51), 2, 16, (1 << 31) // 576 + 1001, 300
