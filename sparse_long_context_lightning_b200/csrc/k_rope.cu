@@ -153,13 +153,17 @@ struct NormRopeArgs {
 // rows a slot at a time, with the next rows' loads in flight; weights and table lie in shared memory, because 32 registers
 // of weights halve the warps of an SM (70 us against 45 for 8192 x 64 rows of 128 dims).  Products and sums go two an
 // instruction.  Small blocks (128 threads, six an SM) wait for each other least: 43.4 us against 44.6 at 256 threads and
-// 70 at 512; a grid of resident blocks with two tables in turn took 55.
-// 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 45.6 us, 5890 GB/s.  2047 x 128 rows of 64, no norm, into
-// their place in rows of 1152 bytes: 17.4 us cold, 3850 GB/s (128-byte pieces of HBM pages; 11 us in the L2).
-// 4099 x 64 rows of 128, layer norm, to codes: 29.6 us, 3440 GB/s, bound by its instructions (about 20 an element: three
-// reductions and a scale a row; 60% of the issue slots at 24 warps an SM, and neither more warps nor larger blocks help).
+// 70 at 512; a grid of resident blocks with two tables in turn took 55.  Six blocks leave a thread 80 registers, at which
+// two chunks a lane spill 4 to 16 bytes: for bf16 that costs less than a block (8192 x 64 rows of 128, RMS norm: 43.0 us
+// against 44.6 at five), for codes, which also hold a row's scale (4 to 60 bytes; at most 12 at five), it costs more (4099 x 64 rows of 128,
+// layer norm: 28.7 us against 27.3 at five; RMS norm 25.5 against 24.2).
+// 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 45.9 us, 5850 GB/s.  2047 x 128 rows of 64, no norm, into
+// their place in rows of 1152 bytes: 15.9 us, 4210 GB/s; neither HBM (29% of its peak) nor the issue slots (36%) are full:
+// it waits for its loads, and its 1024 blocks are little more than the 888 that fit at a time (11.4 us in the L2).
+// 4099 x 64 rows of 128, layer norm, to codes: 27.9 us, 3650 GB/s: about 18 instructions an element (three reductions and a
+// scale a row), 57% of the issue slots at 20 warps an SM; what stalls it is the shuffles and the table in shared memory.
 template <int G, int ITER, int NORM, bool FP8>
-__global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? 6 : 4) k_norm_rope(const NormRopeArgs a) {
+__global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? (FP8 ? 5 : 6) : 4) k_norm_rope(const NormRopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin | weight [D] | bias [D]
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
@@ -452,7 +456,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int far, uint32_t u) {
 // the sums.  A step's few rows are bound by the chain of loads, sums and stores, a prompt's by the rows that an SM holds
 // meanwhile, so registers are kept to 12 blocks an SM (the weights are read when they are used).  16 tokens: 1.9 us with
 // warm caches, 3.4 us cold (2.9 warm with both rows in one warp); 8192 tokens with codes: 10.9 us cold, 2040 GB/s (12.0
-// with 9 blocks an SM).
+// with 9 blocks an SM; inputs in turn 7.4 us, 7.7 with 10 blocks, whose 48 registers spare the 8 bytes that 40 spill).
 template <bool KEYS, bool FP8>
 __global__ void __launch_bounds__(128, 12) k_cache_append(const AppendArgs a) {
   sm100::pdl_wait();
