@@ -506,7 +506,8 @@ int lsa_cache_append(const void* a, int64_t a_ld, int64_t T, int d_qk, int d_v, 
  *   page a power of two from 8 to 65536.  Table entries behind a sequence's last page are not read.  own_len outside [0,
  *   table_ld * page] is clamped and a page id outside [0, n_pages) reads as rows of zeros; lsa_device_status reports either
  *   as LSA_ERR_DEVICE_CHECK.  q, prefix, pages, out 16-byte aligned.  ws: lsa_prefix_attn_workspace_size(B, H) bytes, not
- *   shared by calls that may run at the same time (two streams, two graphs).
+ *   shared by calls that may run at the same time (two streams, two graphs): 19 MB and 2 KiB for each of the B * H query
+ *   rows (4 KiB where H is not a multiple of 128 and B > 1).
  */
 int lsa_prefix_attn(const void* q, int64_t B, int H, int d_qk, int d_v, const void* prefix, int64_t Lp,
                     const void* pages, int64_t n_pages, int page, const int32_t* table, int64_t table_ld,

@@ -84,8 +84,8 @@ struct PaArgs {
   int nP;  // prefix blocks
   float scale_log2;
   int2* seg;      // [items] first and last pair of an item; last = -2: written to out already
-  float2* ws_ml;  // [slots][128] running max (log2 units), sum
-  float* ws_o;    // [slots][128][512]
+  float2* ws_ml;  // [partial rows] running max (log2 units), sum
+  float* ws_o;    // [partial rows][512]
   uint16_t* out;
   float* lse;
 };
@@ -93,7 +93,9 @@ struct PaArgs {
 // A span: the blocks that one pair walks of a tile's prefix or of one query's pages.  What depends on own_len is read
 // once a span (a load a block cost the softmax 780 clocks of 2100).
 // Items: a tile where all rows belong to one query; else a tile's prefix part, and each of its queries' own part.
-// Their numbers rise along the line of blocks, and so does number + pair: the slot of a (item, pair) partial.
+// Of the items that a pair has blocks of, only the first can have begun in an earlier pair.  So a pair has 128 rows for the
+// partial of such an item, and the pair in which an item begins writes to rows of the item's own: row r of the queries has
+// one for the prefix part (or the whole tile) and one for its query's own part.
 // The line counts units: a block is one, and the end of a query's own item (its last products awaited, its rows stored)
 // counts for PA_END more: 45.3 -> 42.2 us for 33 queries of 32 heads with up to 2000 own tokens (2 units: 41.1 there, but
 // 15.2 -> 15.9 where the items are one block each).
@@ -176,6 +178,11 @@ struct Cursor {
     return max(blocks - pos, 0) + (a.multi || b >= 0 ? 0 : blocks_of(a, qlo));
   }
 };
+
+// the partial of query row r from the pair in which its item begins; the pairs' own rows lie ahead (BH < 2^31 - 2^16)
+__device__ __forceinline__ uint32_t part_row(const PaArgs& a, bool own, uint32_t r) {
+  return PA_PAIRS * PA_ROWS + (own ? static_cast<uint32_t>(a.BH) : 0u) + r;
+}
 
 __device__ __forceinline__ int tile_units(const PaArgs& a, int t) {
   Cursor c;
@@ -657,6 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         first = false;
       }
       const int id = c.id(a), left = c.item_left(a);
+      const bool own = a.multi && c.b >= 0;
       c.pos += w - c.real;
       u += w;
       if (u < n) {
@@ -714,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
         }
         if (live && kh == 0 && ch == 0 && a.lse) a.lse[gr] = lt != 0.f ? (m_used + log2f(lt)) * 0.6931471805599453f : -INFINITY;
       } else {
-        const int64_t prow_i = static_cast<int64_t>(id + pair) * PA_ROWS + trow;
+        const int64_t prow_i = seg_pos > 0 ? static_cast<uint32_t>(pair * PA_ROWS + trow) : part_row(a, own, static_cast<uint32_t>(gr));
         #pragma unroll 1
         for (int k = 0; k < 8 && live_rows != 0; ++k) {
           uint32_t o[16];
@@ -766,15 +774,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
 
 // The partials of a row (b, h), from the pairs that shared the row's items, joined by their maxima and sums.
 struct RowParts {
-  int i0, i1, x0, x1, n0, n;  // items, their first pairs, partials of the first, of both
+  int x0, x1, n0, n;  // first pairs of the prefix part (or tile) and of the own part; partials of the first, of both
   bool done;                  // written by the attention itself
   __device__ __forceinline__ void find(const PaArgs& a, uint32_t r) {
     const uint32_t h = static_cast<uint32_t>(a.H);
     const int b = static_cast<int>(r / h), t = static_cast<int>(r / PA_ROWS);
     const int qlo = static_cast<int>(static_cast<uint32_t>(t) * PA_ROWS / h);
     // (written for items that have blocks, so the loads need not wait for the length)
-    i0 = a.multi ? qlo + 2 * t : t;
-    i1 = a.multi ? b + 2 * t + 1 : t;
+    const int i0 = a.multi ? qlo + 2 * t : t, i1 = a.multi ? b + 2 * t + 1 : t;
     const int2 g0 = a.seg[i0], g1 = a.seg[i1];
     const int own = a.own_len ? __ldg(a.own_len + b) : 0;
     if (own < 0 || own > a.cap) atomicExch(&g_prefix_check, 1);
@@ -786,8 +793,9 @@ struct RowParts {
     n0 = any ? max(g0.y - g0.x + 1, 0) : 0;
     n = min(n0 + (a.multi && ob > 0 ? max(g1.y - g1.x + 1, 0) : 0), 2 * PA_PAIRS);
   }
-  __device__ __forceinline__ int64_t row(int i, uint32_t r) const {
-    return static_cast<int64_t>(i < n0 ? i0 + x0 + i : i1 + x1 + i - n0) * PA_ROWS + r % PA_ROWS;
+  __device__ __forceinline__ int64_t row(const PaArgs& a, int i, uint32_t r) const {
+    if (i == 0 || i == n0) return part_row(a, i >= n0, r);
+    return static_cast<uint32_t>((i < n0 ? x0 + i : x1 + i - n0) * PA_ROWS) + r % PA_ROWS;
   }
 };
 __device__ __forceinline__ uint2 pack4(const float4& v, float inv) {
@@ -819,7 +827,7 @@ __global__ void __launch_bounds__(128) k_prefix_combine_rows(const PaArgs a) {
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int b0 = 0; b0 < p.n; b0 += 32) {
     const int i = b0 + lane;
-    const float2 ml = i < p.n ? a.ws_ml[p.row(i, r)] : make_float2(0.f, 0.f);
+    const float2 ml = i < p.n ? a.ws_ml[p.row(a, i, r)] : make_float2(0.f, 0.f);
     const float mn = fmaxf(m, warp_max(ml.y != 0.f ? ml.x : -INFINITY));
     const float old = m == -INFINITY ? 0.f : exp2f(m - mn), w = ml.y != 0.f ? exp2f(ml.x - mn) : 0.f;
     m = mn;
@@ -830,7 +838,7 @@ __global__ void __launch_bounds__(128) k_prefix_combine_rows(const PaArgs a) {
     #pragma unroll 2
     for (int j = 0; j < cnt; ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
-      const float4* src = reinterpret_cast<const float4*>(a.ws_o + p.row(b0 + j, r) * 512);
+      const float4* src = reinterpret_cast<const float4*>(a.ws_o + p.row(a, b0 + j, r) * 512);
       #pragma unroll
       for (int k = 0; k < 4; ++k) add_part(acc[k], wj, src[32 * k + lane]);
     }
@@ -857,13 +865,13 @@ __global__ void __launch_bounds__(128) k_prefix_combine_warps(const PaArgs a) {
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int b0 = 0; b0 < p.n; b0 += 32) {
-    const float2 ml = b0 + lane < p.n ? a.ws_ml[p.row(b0 + lane, r)] : make_float2(0.f, 0.f);
+    const float2 ml = b0 + lane < p.n ? a.ws_ml[p.row(a, b0 + lane, r)] : make_float2(0.f, 0.f);
     const int cnt = min(32, p.n - b0);
     float4 v[U];
     auto load = [&](int j0) {
       #pragma unroll
       for (int k = 0; k < U; ++k)
-        v[k] = j0 + k < cnt ? reinterpret_cast<const float4*>(a.ws_o + p.row(b0 + j0 + k, r) * 512 + c0)[lane]
+        v[k] = j0 + k < cnt ? reinterpret_cast<const float4*>(a.ws_o + p.row(a, b0 + j0 + k, r) * 512 + c0)[lane]
                             : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load(0);
@@ -899,9 +907,9 @@ __global__ void __launch_bounds__(512) k_prefix_combine_few(const PaArgs a) {
   p.find(a, r);
   if (p.done) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float2 ml = tid < p.n ? a.ws_ml[p.row(tid, r)] : make_float2(0.f, 0.f);
+  const float2 ml = tid < p.n ? a.ws_ml[p.row(a, tid, r)] : make_float2(0.f, 0.f);
   auto part = [&](int i) {
-    return i < p.n ? *reinterpret_cast<const float4*>(a.ws_o + p.row(i, r) * 512 + c0 + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return i < p.n ? *reinterpret_cast<const float4*>(a.ws_o + p.row(a, i, r) * 512 + c0 + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   float4 v[U];
   #pragma unroll
@@ -955,7 +963,7 @@ __global__ void __launch_bounds__(512) k_prefix_combine(const PaArgs a) {
   p.find(a, r);
   if (p.done) return;
   const int parts = p.n;
-  auto slot_row = [&](int i) { return p.row(i, r); };
+  auto slot_row = [&](int i) { return p.row(a, i, r); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = tid & 127;
   // the parts' maxima and sums, and the first of the values on their way at the same time
   const float2 ml = tid < parts ? a.ws_ml[slot_row(tid)] : make_float2(0.f, 0.f);
@@ -1032,9 +1040,9 @@ static int make_map_parts(CUtensorMap* m, const void* ptr, int64_t rows, int box
   return LSA_OK;
 }
 
-// Scratch: seg int2 [items] | (max, sum) [slots][128] | O [slots][128][512] fp32, slots = items + 74.
+// Scratch: seg int2 [items] | (max, sum) [partial rows] | O [partial rows][512] fp32.
 struct PrefixLayout {
-  int64_t nT, items, slots;
+  int64_t nT, items, rows;
   bool multi;
   size_t o_ml, o_o, total;
 };
@@ -1043,10 +1051,10 @@ static PrefixLayout prefix_ws_layout(int64_t B, int H) {
   p.nT = cdiv(B * H, PA_ROWS);
   p.multi = H % PA_ROWS != 0 && B > 1;
   p.items = p.multi ? B + 2 * p.nT : p.nT;
-  p.slots = p.items + PA_PAIRS;
+  p.rows = PA_PAIRS * PA_ROWS + (p.multi ? 2 : 1) * B * H;
   p.o_ml = align_up(static_cast<size_t>(p.items) * 8, 256);
-  p.o_o = p.o_ml + static_cast<size_t>(p.slots) * PA_ROWS * 8;
-  p.total = p.o_o + static_cast<size_t>(p.slots) * PA_ROWS * 512 * 4;
+  p.o_o = p.o_ml + align_up(static_cast<size_t>(p.rows) * 8, 256);
+  p.total = p.o_o + static_cast<size_t>(p.rows) * 512 * 4;
   return p;
 }
 

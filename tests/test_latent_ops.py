@@ -131,6 +131,15 @@ def test_prefix_attn_workspace_size(lib):
         assert lib.lsa_prefix_attn_workspace_size(B, H) == bad
 
 
+@pytest.mark.parametrize("B,H", [(1, 128), (1, 5), (16, 128), (33, 32), (256, 8), (4096, 8), (1024, 16), (65535, 1), (3, 65535)])
+def test_prefix_attn_workspace_follows_the_query_rows(lib, B, H):
+    """A row of the queries costs one fp32 row of 512 with its maximum and sum, or two, whatever share of a tile its query
+    fills; beside them the pairs' 74 x 128 rows and 8 bytes for each item."""
+    rows = 74 * 128 + (2 if H % 128 and B > 1 else 1) * B * H
+    tiles = -(-B * H // 128)
+    assert rows * 2056 <= lib.lsa_prefix_attn_workspace_size(B, H) <= rows * 2056 + 8 * (B + 2 * tiles) + 1024
+
+
 def test_packed_forms(lib):
     """The structs that the binding packs are the library's: their sizes are taken, every field lands where the plain call
     has it (each refusal of one field), and another size is refused."""
