@@ -329,6 +329,21 @@ def test_norm_rope_values_that_are_not_finite(norm, D, H, R):
     assert torch.equal(v[inf].isnan(), want[inf].isinf()) and not v[inf][~want[inf].isinf()].any()
 
 
+def test_norm_rope_sums_of_squares_that_overflow():
+    """128 elements of 1e20: their squares' sum is past 32 bits, so the normed values are 0, ahead of weight and bias; of
+    1e18 it is 1.28e38 and the rows are the formula's."""
+    D = 128
+    sign = torch.ones(D, device=DEV)
+    sign[1::2] = -1
+    x = torch.stack([1e20 * sign, 1e18 * sign]).bfloat16().view(2, 1, D)
+    w, b = _weights(_gen(9), "layer", D)
+    for norm, bias in (("rms", None), ("layer", b)):
+        y = torch.empty_like(x)
+        lsa.lsa_norm_rope(x, y, norm=norm, weight=w, bias=bias)
+        assert torch.equal(y[0, 0], bias.bfloat16() if bias is not None else torch.zeros_like(y[0, 0]))
+        check_rows(y[1:], norm64(x[1:], norm, w, bias, 1e-6))
+
+
 @pytest.mark.parametrize("k_norm", ["none", "rms", "layer"])
 @pytest.mark.parametrize("d_I", [32, 128])
 def test_cache_append_values_that_are_not_finite(k_norm, d_I):
