@@ -774,8 +774,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PA_THREADS, 1)
 
 // The partials of a row (b, h), from the pairs that shared the row's items, joined by their maxima and sums.
 struct RowParts {
-  int x0, x1, n0, n;  // first pairs of the prefix part (or tile) and of the own part; partials of the first, of both
-  bool done;                  // written by the attention itself
+  int n0, n;           // partials of the prefix part (or tile), and of it and the own part
+  uint32_t f0, f1;     // where the first partial of either lies,
+  uint32_t c0, c1;     // and the others: partial i at c + i * 128
+  bool done;           // written by the attention itself
   __device__ __forceinline__ void find(const PaArgs& a, uint32_t r) {
     const uint32_t h = static_cast<uint32_t>(a.H);
     const int b = static_cast<int>(r / h), t = static_cast<int>(r / PA_ROWS);
@@ -786,16 +788,19 @@ struct RowParts {
     const int own = a.own_len ? __ldg(a.own_len + b) : 0;
     if (own < 0 || own > a.cap) atomicExch(&g_prefix_check, 1);
     const int ob = Cursor::blocks_of(a, b);
-    x0 = g0.x;
-    x1 = g1.x;
     const bool any = (a.multi ? a.nP : a.nP + ob) > 0;
     done = any && g0.y == -2;
     n0 = any ? max(g0.y - g0.x + 1, 0) : 0;
     n = min(n0 + (a.multi && ob > 0 ? max(g1.y - g1.x + 1, 0) : 0), 2 * PA_PAIRS);
+    f0 = part_row(a, false, r);
+    f1 = part_row(a, true, r);
+    c0 = static_cast<uint32_t>(g0.x * PA_ROWS) + r % PA_ROWS;
+    c1 = static_cast<uint32_t>((g1.x - n0) * PA_ROWS) + r % PA_ROWS;
   }
-  __device__ __forceinline__ int64_t row(const PaArgs& a, int i, uint32_t r) const {
-    if (i == 0 || i == n0) return part_row(a, i >= n0, r);
-    return static_cast<uint32_t>((i < n0 ? x0 + i : x1 + i - n0) * PA_ROWS) + r % PA_ROWS;
+  __device__ __forceinline__ int64_t row(int i) const {
+    uint32_t v = (i < n0 ? c0 : c1) + static_cast<uint32_t>(i * PA_ROWS);
+    v = i == 0 ? f0 : v;
+    return i == n0 ? f1 : v;
   }
 };
 __device__ __forceinline__ uint2 pack4(const float4& v, float inv) {
@@ -827,7 +832,7 @@ __global__ void __launch_bounds__(128) k_prefix_combine_rows(const PaArgs a) {
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int b0 = 0; b0 < p.n; b0 += 32) {
     const int i = b0 + lane;
-    const float2 ml = i < p.n ? a.ws_ml[p.row(a, i, r)] : make_float2(0.f, 0.f);
+    const float2 ml = i < p.n ? a.ws_ml[p.row(i)] : make_float2(0.f, 0.f);
     const float mn = fmaxf(m, warp_max(ml.y != 0.f ? ml.x : -INFINITY));
     const float old = m == -INFINITY ? 0.f : exp2f(m - mn), w = ml.y != 0.f ? exp2f(ml.x - mn) : 0.f;
     m = mn;
@@ -838,7 +843,7 @@ __global__ void __launch_bounds__(128) k_prefix_combine_rows(const PaArgs a) {
     #pragma unroll 2
     for (int j = 0; j < cnt; ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
-      const float4* src = reinterpret_cast<const float4*>(a.ws_o + p.row(a, b0 + j, r) * 512);
+      const float4* src = reinterpret_cast<const float4*>(a.ws_o + p.row(b0 + j) * 512);
       #pragma unroll
       for (int k = 0; k < 4; ++k) add_part(acc[k], wj, src[32 * k + lane]);
     }
@@ -865,13 +870,13 @@ __global__ void __launch_bounds__(128) k_prefix_combine_warps(const PaArgs a) {
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int b0 = 0; b0 < p.n; b0 += 32) {
-    const float2 ml = b0 + lane < p.n ? a.ws_ml[p.row(a, b0 + lane, r)] : make_float2(0.f, 0.f);
+    const float2 ml = b0 + lane < p.n ? a.ws_ml[p.row(b0 + lane)] : make_float2(0.f, 0.f);
     const int cnt = min(32, p.n - b0);
     float4 v[U];
     auto load = [&](int j0) {
       #pragma unroll
       for (int k = 0; k < U; ++k)
-        v[k] = j0 + k < cnt ? reinterpret_cast<const float4*>(a.ws_o + p.row(a, b0 + j0 + k, r) * 512 + c0)[lane]
+        v[k] = j0 + k < cnt ? reinterpret_cast<const float4*>(a.ws_o + p.row(b0 + j0 + k) * 512 + c0)[lane]
                             : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load(0);
@@ -894,7 +899,7 @@ __global__ void __launch_bounds__(128) k_prefix_combine_warps(const PaArgs a) {
 // every load of a row on its way before the weights are formed.  The whole call against one block a row (below), in a
 // graph: 128 rows of 74 partials 16.9 against 18.1 us, of 56 16.2 against 17.1, of 48 16.0 against 16.6, of 40 16.0 against
 // 15.2, of 8 14.0 against 12.8; 64 rows of 74 16.0 against 18.5, of 48 15.5 against 16.0.
-__global__ void __launch_bounds__(512) k_prefix_combine_few(const PaArgs a) {
+__global__ void __launch_bounds__(512, 3) k_prefix_combine_few(const PaArgs a) {
   constexpr int W = 16, U = 5;
   __shared__ float wt[2 * PA_PAIRS];
   __shared__ float red[2 * W];
@@ -907,9 +912,9 @@ __global__ void __launch_bounds__(512) k_prefix_combine_few(const PaArgs a) {
   p.find(a, r);
   if (p.done) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float2 ml = tid < p.n ? a.ws_ml[p.row(a, tid, r)] : make_float2(0.f, 0.f);
+  const float2 ml = tid < p.n ? a.ws_ml[p.row(tid)] : make_float2(0.f, 0.f);
   auto part = [&](int i) {
-    return i < p.n ? *reinterpret_cast<const float4*>(a.ws_o + p.row(a, i, r) * 512 + c0 + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return i < p.n ? *reinterpret_cast<const float4*>(a.ws_o + p.row(i) * 512 + c0 + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   float4 v[U];
   #pragma unroll
@@ -963,7 +968,7 @@ __global__ void __launch_bounds__(512) k_prefix_combine(const PaArgs a) {
   p.find(a, r);
   if (p.done) return;
   const int parts = p.n;
-  auto slot_row = [&](int i) { return p.row(a, i, r); };
+  auto slot_row = [&](int i) { return p.row(i); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = tid & 127;
   // the parts' maxima and sums, and the first of the values on their way at the same time
   const float2 ml = tid < parts ? a.ws_ml[slot_row(tid)] : make_float2(0.f, 0.f);
