@@ -506,7 +506,7 @@ int lsa_cache_append(const void* a, int64_t a_ld, int64_t T, int d_qk, int d_v, 
  *   give 0.0016 to 0.0017.
  *   A query without any key gives out = 0, lse = -inf.  Each tile of 128 query rows walks the whole prefix, twice a block
  *   (as keys and as values); the tiles walk it together, so that all but about one pass come from the L2 (16 queries of
- *   128 heads behind 131072 rows read 177 MB from HBM, where q, prefix and own rows are 157 MB).
+ *   128 heads behind 131072 rows read about 178 MB from HBM, where q, prefix and own rows are 157 MB).
  *   Several tokens of one sequence (speculative or chunked decoding) are several queries with the same table row and
  *   growing own_len.
  *   q [B, H, 576] bf16, prefix [Lp, 576] bf16, pages [n_pages, page, 576] bf16, table int32 [B, table_ld], own_len int32

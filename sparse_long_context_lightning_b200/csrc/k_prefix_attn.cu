@@ -19,10 +19,11 @@
 // blocks (N = 64, A read again for each, 22.6 clocks a key and SM against 17.0) the decode batch below took 529 us against
 // 470, both before pairs walked in step.  Prefetching blocks into the L2 ahead of the loads gained 2.5 us for one query
 // behind 131072 rows and cost the other cases 0.2 to 0.4 us: left out.
-// 16 queries of 128 heads behind 131072 rows: 400 us (1460 TFLOP/s, matrix units busy 86% of the time), 478 us when run
-// for seconds, where the power limit holds the clock (1225 TFLOP/s; cuBLAS sustains 1385 there).  64 queries behind 32749
-// rows: 405 us, 481 sustained.  One query of 128 heads behind 131072 rows: 49 us, of which 28 in the loop (5.4 TB/s from
-// HBM) and 21 in start, partials and join.  4 queries of 16 heads behind 1024 rows: 13 us, all latency.
+// 16 queries of 128 heads behind 131072 rows: 400 us (1460 TFLOP/s, matrix units busy 84% of the time), 470 to 485 us when
+// run for seconds, where the power limit holds the clock (1205 to 1245 TFLOP/s; cuBLAS sustains 1385 there).  64 queries
+// behind 32749 rows: 403 us, 470 to 487 sustained.  One query of 128 heads behind 131072 rows: 46 to 49 us in a graph, 54
+// through a call, of which 28 in the loop (5.4 TB/s from HBM) and 21 in start, partials and join.  4 queries of 16 heads
+// behind 1024 rows: 13 us, all latency.
 //
 // Work is cut evenly: the blocks of all tiles, in order, are one line that 74 pairs divide; a tile that spans pairs
 // leaves partial sums (fp32) that a second kernel joins, and one that lies in a pair is written at once (74 queries of 128

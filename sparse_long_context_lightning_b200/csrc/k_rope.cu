@@ -158,10 +158,10 @@ struct NormRopeArgs {
 // against 44.6 at five), for codes, which also hold a row's scale (4 to 60 bytes; at most 12 at five), it costs more (4099 x 64 rows of 128,
 // layer norm: 28.7 us against 27.3 at five; RMS norm 25.5 against 24.2).
 // 8192 x 64 rows of 128 dims, RMS norm, whole heads rotated: 45.9 us, 5850 GB/s.  2047 x 128 rows of 64, no norm, into
-// their place in rows of 1152 bytes: 15.9 us, 4210 GB/s; neither HBM (29% of its peak) nor the issue slots (36%) are full:
+// their place in rows of 1152 bytes: 15.9 us, 4210 GB/s; neither HBM (28% of its peak) nor the issue slots (34%) are full:
 // it waits for its loads, and its 1024 blocks are little more than the 888 that fit at a time (11.4 us in the L2).
 // 4099 x 64 rows of 128, layer norm, to codes: 27.9 us, 3650 GB/s: about 18 instructions an element (three reductions and a
-// scale a row), 57% of the issue slots at 20 warps an SM; what stalls it is the shuffles and the table in shared memory.
+// scale a row), 55% of the issue slots at 20 warps an SM; what stalls it is the shuffles and the table in shared memory.
 template <int G, int ITER, int NORM, bool FP8>
 __global__ void __launch_bounds__(NR_THREADS, ITER <= 2 ? (FP8 ? 5 : 6) : 4) k_norm_rope(const NormRopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];  // [tokens][R / 2] cos, sin | weight [D] | bias [D]
