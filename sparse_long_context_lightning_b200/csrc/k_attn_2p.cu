@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(A2_THREADS, 1)
   constexpr int Q_STEP = A2_THREADS / 32 - A2_GATHER_WARPS;
   for (int kb = q_first; kb < A2_QSLOTS; kb += Q_STEP) mbar_init(&q_slot[kb], 1);
   if (q_first < A2_QSLOTS) fence_mbar_init();
+  __syncwarp();  // the allocation below is the whole warp's
   if (warp == A2_LOGIT_WARP0) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
